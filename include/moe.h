@@ -15,6 +15,8 @@
  *   moe_combine    gate-weighted sum of each token's expert outputs (un-permute)
  *   moe_expert_ffn_combine  the last two fused, for top-1 routing in bf16
  *   moe_forward    all of the above on one stream
+ * Beside it: the training pass (moe_forward_train, moe_backward), and the norm in front of the
+ * layer with the layer's 8-bit form (moe_rmsnorm ... moe_expert_ffn_fp8).
  *
  * Conventions for every call
  *  - All pointers are DEVICE pointers unless stated, owned by the caller, and must
@@ -356,6 +358,126 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const void* w_gate
                         const void* state, const float* dy, float w_importance, float w_load,
                         float* dx, float* dw_gate, float* dw_noise, float* dlogit_bias, float* dw1,
                         float* dw2, float* dgates, float* losses, void* ws, moe_stream_t stream);
+
+/* ---------------------------------------------------- norm and 8-bit operators
+ * The block around the layer as it is served in 8 bits: a root-mean-square norm that adds
+ * the residual and writes its rows in 16 and in 8 bits, products of 8-bit operands (dense,
+ * and grouped by expert), and the expert FFN on them.  The pages have no counterpart.
+ *
+ * 8-bit format ("fp8" in the names): e4m3 values q (one byte, bit layout of OCP FP8 E4M3,
+ * no infinities) with fp32 scales s; a value reads back as q * s.
+ *   rows     q [rows, d], scale [ceil(d/128), rows]: one scale for each 128 consecutive
+ *            values of a row (the last block may be shorter), block-major so that a warp
+ *            reads the scales of 32 rows at once
+ *   weights  q [groups, N, K], scale [groups, ceil(N/128), ceil(K/128)]: one scale for each
+ *            128 x 128 block
+ * Quantising: with a = max|v| over the block, s = max(a / 448, 2^-126) and q = 448 v / a
+ * rounded to nearest even (the quotient correctly rounded in fp32 first for values given in
+ * memory, within 2^-23 of itself for values computed by the same kernel).  A block that
+ * holds a NaN or an infinity reads back as NaN throughout; a block of zeros as zeros.
+ * Scales in other forms are read as they are: any fp32 numbers, powers of two among them. */
+
+/* Root-mean-square norm of rows, with the residual added first:
+ *   r = x + residual (rounded to dtype; x where residual is NULL),
+ *   rstd = 1 / sqrt(mean(r^2) + eps),  y = r * rstd * weight
+ *  dtype        moe_dtype of x, residual, weight, residual_out and y
+ *  x, residual  [rows, d] in; residual or NULL
+ *  weight       [d] in
+ *  residual_out [rows, d] out or NULL: r.  May be x or residual itself.
+ *  y            [rows, d] out or NULL
+ *  y_q, y_scale [rows, d] e4m3 and [ceil(d/128), rows] fp32 out, or both NULL: y in 8 bits,
+ *               quantised from the fp32 values (not from the rounded y); d % 16 == 0
+ *  rstd         [rows] fp32 out or NULL (the backward needs it)
+ * d a multiple of 8, at most 16384; at least one output; eps >= 0.  rows == 0 launches
+ * nothing.  r^2 must not overflow fp32 (|r| below 1e18 or so), as usual for this norm. */
+moe_status moe_rmsnorm(int64_t rows, int32_t d, int32_t dtype, float eps, const void* x,
+                       const void* residual, const void* weight, void* residual_out, void* y,
+                       void* y_q, float* y_scale, float* rstd, moe_stream_t stream);
+
+/* Bytes of workspace moe_rmsnorm_backward needs for dweight; 0 for unsupported sizes. */
+size_t moe_rmsnorm_backward_workspace_size(int64_t rows, int32_t d);
+
+/* Gradients of moe_rmsnorm: with xhat = r * rstd,
+ *   dx = dresidual + rstd * (weight * dy - xhat * mean(weight * dy * xhat)),
+ *   dweight = sum over rows of dy * xhat
+ *  dtype      moe_dtype of r and weight
+ *  r          [rows, d] in: the forward's residual_out, or x where there was no residual
+ *  rstd       [rows] fp32 in, from the forward
+ *  dy         [rows, d] fp32 in: gradient of y (moe_backward's dx is one)
+ *  dresidual  [rows, d] fp32 in or NULL: gradient that reaches r past the norm
+ *  dx         [rows, d] fp32 out: gradient of r, that is of x and of residual alike; may be
+ *             dresidual itself
+ *  dweight    [d] fp32 out or NULL; summed in a fixed order
+ *  ws         moe_rmsnorm_backward_workspace_size bytes, 16-byte aligned, or NULL without
+ *             dweight (contents do not matter)
+ * rows == 0 zeroes dweight. */
+moe_status moe_rmsnorm_backward(int64_t rows, int32_t d, int32_t dtype, const void* r,
+                                const void* weight, const float* rstd, const float* dy,
+                                const float* dresidual, float* dx, float* dweight, void* ws,
+                                moe_stream_t stream);
+
+/* Rows x [rows, d] (dtype) as e4m3 with block scales.  d a multiple of 16. */
+moe_status moe_quantize_rows_fp8(int64_t rows, int32_t d, int32_t dtype, const void* x, void* q,
+                                 float* scale, moe_stream_t stream);
+
+/* Weights w [groups, N, K] (dtype) as e4m3 with a scale for each 128 x 128 block.  K a
+ * multiple of 16.  Weight preparation, run once before the calls that use it. */
+moe_status moe_quantize_weights_fp8(int64_t groups, int32_t N, int32_t K, int32_t dtype,
+                                    const void* w, void* q, float* scale, moe_stream_t stream);
+
+/* Dispatch of quantised token rows: permuted row s is token row perm_src[s] / k of x_q, with
+ * its scales, for s < offsets[E] (the copy that moe_permute makes of x, in 8 bits; run
+ * moe_permute with x_perm NULL for the index arrays).
+ *  x_q [T, d_model] e4m3, x_scale [ceil(d_model/128), T] in
+ *  perm_src [T*k], offsets [E+1] int32 in, as written by moe_permute
+ *  xq_perm [T*k, d_model], xs_perm [ceil(d_model/128), T*k] out; rows >= offsets[E] are
+ *  left untouched
+ * bf16 layers.  A perm_src entry outside [0, T*k) sets MOE_DEVERR_SLOT and leaves its row;
+ * offsets[E] outside [0, T*k] sets MOE_DEVERR_OFFSETS and nothing is copied. */
+moe_status moe_gather_rows_fp8(const moe_config* cfg, const void* x_q, const float* x_scale,
+                               const int32_t* perm_src, const int32_t* offsets, void* xq_perm,
+                               float* xs_perm, void* ws, moe_stream_t stream);
+
+/* Product of 8-bit operands, out = A . B^T:
+ *   out[m, n] = sum_b a_scale[b, m] b_scale[n/128, b] sum_{k in block b} a_q[m, k] b_q[n, k]
+ * The inner sums are formed by the tensor cores in fp32, the sum over blocks by fp32
+ * multiply-adds.
+ *  a_q [M, K], a_scale [ceil(K/128), M];  b_q [N, K], b_scale [ceil(N/128), ceil(K/128)]
+ *  out [M, N] fp32 or bf16 (out_dtype; each fp32 sum rounded once)
+ *  ws  at least 256 bytes of a workspace as for the step calls (its device error word)
+ * N a multiple of 8, K a multiple of 16.  M == 0 launches nothing. */
+moe_status moe_matmul_fp8(int64_t M, int32_t N, int32_t K, const void* a_q, const float* a_scale,
+                          const void* b_q, const float* b_scale, void* out, int32_t out_dtype,
+                          void* ws, moe_stream_t stream);
+
+/* The product by row groups: rows [offsets[g], offsets[g+1]) of a_q times weight block g.
+ *  a_q [rows, K], a_scale [ceil(K/128), rows]; offsets [groups+1] int32 in, non-decreasing
+ *  in [0, rows] (else MOE_DEVERR_OFFSETS and no output)
+ *  b_q [groups, N, K], b_scale [groups, ceil(N/128), ceil(K/128)]
+ *  out [rows, N] fp32 or bf16; rows outside [offsets[0], offsets[groups]) are left
+ *  untouched
+ * Groups may be empty; groups <= 1024.  N, K, ws as moe_matmul_fp8. */
+moe_status moe_grouped_matmul_fp8(int64_t rows, int32_t N, int32_t K, int32_t groups,
+                                  const void* a_q, const float* a_scale, const int32_t* offsets,
+                                  const void* b_q, const float* b_scale, void* out,
+                                  int32_t out_dtype, void* ws, moe_stream_t stream);
+
+/* moe_expert_ffn in 8 bits:
+ *   h[s] = act(x[s] . W1_e^T) in e4m3 with block scales,  y_perm[s] = h[s] . W2_e^T
+ * for offsets[e] <= s < offsets[e+1]; the activation and the quantisation of h (from the fp32
+ * sums) run in the first product's epilogue.
+ *  x_q [T*k, d_model], x_scale [ceil(d_model/128), T*k] in, as moe_gather_rows_fp8 writes them
+ *  w1_q [E, d_ff, d_model], w1_scale; w2_q [E, d_model, d_ff], w2_scale in, as
+ *  moe_quantize_weights_fp8 writes them
+ *  h_q [T*k, d_ff], h_scale [ceil(d_ff/128), T*k] out (rows < offsets[E])
+ *  y_perm [T*k, d_model] fp32 out (rows < offsets[E]), as moe_combine takes it
+ * bf16 layers without hidden_f16 (else MOE_ERR_UNSUPPORTED); d_model and d_ff multiples of
+ * 64, E <= 256 as for every bf16 layer.  Inference only: moe_backward differentiates the
+ * 16-bit layer. */
+moe_status moe_expert_ffn_fp8(const moe_config* cfg, const void* x_q, const float* x_scale,
+                              const int32_t* offsets, const void* w1_q, const float* w1_scale,
+                              const void* w2_q, const float* w2_scale, void* h_q, float* h_scale,
+                              void* y_perm, void* ws, moe_stream_t stream);
 
 /* Synchronises `stream`, then reads the device error word in `ws` into *device_error
  * (may be NULL) and clears it.  Returns MOE_OK if no bit was set, MOE_ERR_DEVICE if

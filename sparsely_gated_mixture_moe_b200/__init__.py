@@ -29,6 +29,7 @@ def _load():
     lib = ctypes.CDLL(_LIB_PATH)
     P = ctypes.c_void_p
     C = ctypes.POINTER(MoEConfig)
+    I32, I64, F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "moe_capacity": (ctypes.c_int64, [C]),
@@ -56,6 +57,15 @@ def _load():
         "moe_backward": (ctypes.c_int, [C] + [P] * 13 + [ctypes.c_float, ctypes.c_float] +
                          [P] * 10),
         "moe_wait_timeout_check": (ctypes.c_int, [P, P]),
+        "moe_rmsnorm": (ctypes.c_int, [I64, I32, I32, F32] + [P] * 9),
+        "moe_rmsnorm_backward_workspace_size": (ctypes.c_size_t, [I64, I32]),
+        "moe_rmsnorm_backward": (ctypes.c_int, [I64, I32, I32] + [P] * 9),
+        "moe_quantize_rows_fp8": (ctypes.c_int, [I64, I32, I32] + [P] * 4),
+        "moe_quantize_weights_fp8": (ctypes.c_int, [I64, I32, I32, I32] + [P] * 4),
+        "moe_gather_rows_fp8": (ctypes.c_int, [C] + [P] * 8),
+        "moe_matmul_fp8": (ctypes.c_int, [I64, I32, I32] + [P] * 5 + [I32, P, P]),
+        "moe_grouped_matmul_fp8": (ctypes.c_int, [I64, I32, I32, I32] + [P] * 6 + [I32, P, P]),
+        "moe_expert_ffn_fp8": (ctypes.c_int, [C] + [P] * 12),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -288,6 +298,200 @@ def prepare_weights(cfg: MoEConfig, weights: dict, stream=None) -> dict:
     return out
 
 
+# ------------------------------------------------------- norm and 8-bit operators
+
+_F8 = torch.float8_e4m3fn
+_KIND = {torch.float32: DTYPE["f32"], torch.bfloat16: DTYPE["bf16"]}
+
+
+def scale_blocks(n: int) -> int:
+    """Blocks of 128 that n values take (the last may be shorter)."""
+    return -(-n // 128)
+
+
+def _kind(t: torch.Tensor, what: str) -> int:
+    try:
+        return _KIND[t.dtype]
+    except KeyError:
+        raise ValueError("%s must be bf16 or fp32, not %s" % (what, t.dtype)) from None
+
+
+def _need(what: str, t, shape, dtype, device: int):
+    """The device pointer of a contiguous CUDA tensor of this shape and type on `device`."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s must be %s %s, not %s %s" % (what, dtype, list(shape), t.dtype,
+                                                          list(t.shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be a CUDA tensor on device %d, where the call runs"
+                         % (what, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _matrix(what: str, t, ndim: int = 2):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, not %d" % (what, ndim, t.dim()))
+    return t.shape
+
+
+def _workspace_ptr(ws, device: int, least: int = 256):
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor on device %d" % device)
+    if ws.numel() * ws.element_size() < least:
+        raise ValueError("ws holds %d bytes, %d are needed" % (ws.numel() * ws.element_size(), least))
+    return ws.data_ptr()
+
+
+def moe_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, y_q=None,
+                y_scale=None, rstd=None, stream=None):
+    """r = x + residual (to residual_out), y = r / sqrt(mean(r^2) + eps) * weight into y (x's
+    type) and / or (y_q, y_scale) (e4m3 with block scales); rstd [rows] for the backward."""
+    rows, d = _matrix("x", x)
+    t, dev = x.dtype, torch.cuda.current_device()
+    kind, shape = _kind(x, "x"), x.shape
+    _check(lib.moe_rmsnorm(rows, d, kind, eps, _need("x", x, shape, t, dev),
+                           _need("residual", residual, shape, t, dev),
+                           _need("weight", weight, (d,), t, dev),
+                           _need("residual_out", residual_out, shape, t, dev),
+                           _need("y", y, shape, t, dev), _need("y_q", y_q, shape, _F8, dev),
+                           _need("y_scale", y_scale, (scale_blocks(d), rows), torch.float32, dev),
+                           _need("rstd", rstd, (rows,), torch.float32, dev), _stream(stream)),
+           "moe_rmsnorm")
+
+
+def rmsnorm_backward_workspace(rows: int, d: int, device="cuda") -> torch.Tensor:
+    """A device workspace for moe_rmsnorm_backward."""
+    n = int(lib.moe_rmsnorm_backward_workspace_size(rows, d))
+    if n == 0:
+        raise MoEError(2, "norm of %d rows of %d values" % (rows, d))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_rmsnorm_backward(r, weight, rstd, dy, dx, ws=None, dresidual=None, dweight=None,
+                         stream=None):
+    """Gradients of moe_rmsnorm: dx of r (so of x and of the residual), dweight of weight (then
+    ws is needed).  r is the forward's residual_out, or x where there was no residual."""
+    rows, d = _matrix("r", r)
+    dev, f32, shape = torch.cuda.current_device(), torch.float32, r.shape
+    kind = _kind(r, "r")
+    least = int(lib.moe_rmsnorm_backward_workspace_size(rows, d)) if dweight is not None else 0
+    _check(lib.moe_rmsnorm_backward(rows, d, kind, _need("r", r, shape, r.dtype, dev),
+                                    _need("weight", weight, (d,), r.dtype, dev),
+                                    _need("rstd", rstd, (rows,), f32, dev),
+                                    _need("dy", dy, shape, f32, dev),
+                                    _need("dresidual", dresidual, shape, f32, dev),
+                                    _need("dx", dx, shape, f32, dev),
+                                    _need("dweight", dweight, (d,), f32, dev),
+                                    None if ws is None else _workspace_ptr(ws, dev, least),
+                                    _stream(stream)), "moe_rmsnorm_backward")
+
+
+def moe_quantize_rows_fp8(x, q, scale, stream=None):
+    """Rows x [rows, d] (bf16 or fp32) as e4m3 q with scale [scale_blocks(d), rows]."""
+    rows, d = _matrix("x", x)
+    dev, kind = torch.cuda.current_device(), _kind(x, "x")
+    _check(lib.moe_quantize_rows_fp8(rows, d, kind, _need("x", x, x.shape, x.dtype, dev),
+                                     _need("q", q, x.shape, _F8, dev),
+                                     _need("scale", scale, (scale_blocks(d), rows), torch.float32,
+                                           dev), _stream(stream)), "moe_quantize_rows_fp8")
+
+
+def moe_quantize_weights_fp8(w, q, scale, stream=None):
+    """Weights w [N, K] or [groups, N, K] as e4m3 q (same shape) with a scale for each block
+    of 128 x 128, [.., scale_blocks(N), scale_blocks(K)]."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a tensor of two or three dimensions")
+    N, K = w.shape[-2:]
+    groups = w.shape[0] if w.dim() == 3 else 1
+    dev, kind = torch.cuda.current_device(), _kind(w, "w")
+    sshape = (*w.shape[:-2], scale_blocks(N), scale_blocks(K))
+    _check(lib.moe_quantize_weights_fp8(groups, N, K, kind, _need("w", w, w.shape, w.dtype, dev),
+                                        _need("q", q, w.shape, _F8, dev),
+                                        _need("scale", scale, sshape, torch.float32, dev),
+                                        _stream(stream)), "moe_quantize_weights_fp8")
+
+
+def quantize_weights(w, stream=None):
+    """(q, scale) of weights w [N, K] or [groups, N, K]: moe_quantize_weights_fp8 into new
+    tensors."""
+    q = torch.empty(w.shape, dtype=_F8, device=w.device)
+    scale = torch.empty(*w.shape[:-2], scale_blocks(w.shape[-2]), scale_blocks(w.shape[-1]),
+                        dtype=torch.float32, device=w.device)
+    moe_quantize_weights_fp8(w, q, scale, stream=stream)
+    return q, scale
+
+
+def moe_gather_rows_fp8(cfg, x_q, x_scale, perm_src, offsets, xq_perm, xs_perm, ws, stream=None):
+    """Permuted row s < offsets[E] is token row perm_src[s] // k of x_q, with its scales."""
+    T, d, n, dev = cfg.T, cfg.d_model, cfg.T * cfg.k, torch.cuda.current_device()
+    f32, i32, b = torch.float32, torch.int32, scale_blocks(d)
+    _check(lib.moe_gather_rows_fp8(ctypes.byref(cfg), _need("x_q", x_q, (T, d), _F8, dev),
+                                   _need("x_scale", x_scale, (b, T), f32, dev),
+                                   _need("perm_src", perm_src, (n,), i32, dev),
+                                   _need("offsets", offsets, (cfg.E + 1,), i32, dev),
+                                   _need("xq_perm", xq_perm, (n, d), _F8, dev),
+                                   _need("xs_perm", xs_perm, (b, n), f32, dev),
+                                   _workspace_ptr(ws, dev), _stream(stream)),
+           "moe_gather_rows_fp8")
+
+
+def moe_matmul_fp8(a_q, a_scale, b_q, b_scale, out, ws, stream=None):
+    """out [M, N] (fp32 or bf16) = a . b^T of e4m3 a_q [M, K] and b_q [N, K] with their block
+    scales [scale_blocks(K), M] and [scale_blocks(N), scale_blocks(K)]."""
+    M, K = _matrix("a_q", a_q)
+    N, dev, f32 = _matrix("b_q", b_q)[0], torch.cuda.current_device(), torch.float32
+    kb, kind = scale_blocks(K), _kind(out, "out")
+    _check(lib.moe_matmul_fp8(M, N, K, _need("a_q", a_q, (M, K), _F8, dev),
+                              _need("a_scale", a_scale, (kb, M), f32, dev),
+                              _need("b_q", b_q, (N, K), _F8, dev),
+                              _need("b_scale", b_scale, (scale_blocks(N), kb), f32, dev),
+                              _need("out", out, (M, N), out.dtype, dev), kind,
+                              _workspace_ptr(ws, dev), _stream(stream)), "moe_matmul_fp8")
+
+
+def moe_grouped_matmul_fp8(a_q, a_scale, offsets, b_q, b_scale, out, ws, stream=None):
+    """Rows [offsets[g], offsets[g+1]) of out = those of a . b[g]^T; b_q [groups, N, K]."""
+    rows, K = _matrix("a_q", a_q)
+    groups, N, _ = _matrix("b_q", b_q, 3)
+    dev, f32, kb, kind = torch.cuda.current_device(), torch.float32, scale_blocks(K), _kind(out, "out")
+    _check(lib.moe_grouped_matmul_fp8(rows, N, K, groups, _need("a_q", a_q, (rows, K), _F8, dev),
+                                      _need("a_scale", a_scale, (kb, rows), f32, dev),
+                                      _need("offsets", offsets, (groups + 1,), torch.int32, dev),
+                                      _need("b_q", b_q, (groups, N, K), _F8, dev),
+                                      _need("b_scale", b_scale, (groups, scale_blocks(N), kb), f32,
+                                            dev),
+                                      _need("out", out, (rows, N), out.dtype, dev), kind,
+                                      _workspace_ptr(ws, dev), _stream(stream)),
+           "moe_grouped_matmul_fp8")
+
+
+def moe_expert_ffn_fp8(cfg, x_q, x_scale, offsets, w1_q, w1_scale, w2_q, w2_scale, h_q, h_scale,
+                       y_perm, ws, stream=None):
+    """moe_expert_ffn on e4m3 rows and weights; h in e4m3 too, y_perm fp32."""
+    n, d, f, E, dev = cfg.T * cfg.k, cfg.d_model, cfg.d_ff, cfg.E, torch.cuda.current_device()
+    f32, db, fb = torch.float32, scale_blocks(d), scale_blocks(f)
+    _check(lib.moe_expert_ffn_fp8(ctypes.byref(cfg), _need("x_q", x_q, (n, d), _F8, dev),
+                                  _need("x_scale", x_scale, (db, n), f32, dev),
+                                  _need("offsets", offsets, (E + 1,), torch.int32, dev),
+                                  _need("w1_q", w1_q, (E, f, d), _F8, dev),
+                                  _need("w1_scale", w1_scale, (E, fb, db), f32, dev),
+                                  _need("w2_q", w2_q, (E, d, f), _F8, dev),
+                                  _need("w2_scale", w2_scale, (E, db, fb), f32, dev),
+                                  _need("h_q", h_q, (n, f), _F8, dev),
+                                  _need("h_scale", h_scale, (fb, n), f32, dev),
+                                  _need("y_perm", y_perm, (n, d), f32, dev),
+                                  _workspace_ptr(ws, dev), _stream(stream)), "moe_expert_ffn_fp8")
+
+
 def last_launch_count() -> int:
     """Kernels queued by the most recent successful call on this thread."""
     return int(lib.moe_last_launch_count())
@@ -332,4 +536,7 @@ __all__ = ["ACT", "DEVERR", "DTYPE", "GATING", "MoEConfig", "MoEError", "MoELaye
            "moe_expert_ffn_grouped",
            "prepare_weights", "moe_permute_noalloc", "moe_expert_ffn_combine", "fused_combine",
            "moe_expert_ffn_gather", "moe_expert_ffn_combine_gather", "train_state",
-           "backward_workspace", "moe_forward_train", "moe_backward"]
+           "backward_workspace", "moe_forward_train", "moe_backward", "moe_rmsnorm",
+           "moe_rmsnorm_backward", "rmsnorm_backward_workspace", "moe_quantize_rows_fp8",
+           "moe_quantize_weights_fp8", "quantize_weights", "scale_blocks", "moe_gather_rows_fp8",
+           "moe_matmul_fp8", "moe_grouped_matmul_fp8", "moe_expert_ffn_fp8"]

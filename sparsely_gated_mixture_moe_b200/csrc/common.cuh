@@ -166,9 +166,22 @@ __device__ __forceinline__ void tc_mma_f16kind(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
+// The same with 8-bit inputs (e4m3 as the instruction descriptor says), K = 32.
+__device__ __forceinline__ void tc_mma_f8kind(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor of kind::f16 with A and B of one 16-bit type (both K-major)
 // and fp32 D.  bits 4-5 D format (1 = f32), 7-9 A format and 10-12 B format (0 = fp16,
 // 1 = bf16; always equal here), 15/16 A/B major (0 = K-major), 17-22 N >> 3, 24-28 M >> 4.
+// kind::f8f6f4 uses the same fields; 0 in the format fields is e4m3 there.
+constexpr uint32_t kFmtE4M3 = 0;
 constexpr uint32_t kFmtF16 = 0;
 constexpr uint32_t kFmtBF16 = 1;
 __host__ __device__ constexpr uint32_t idesc_f32acc(int M, int N, uint32_t ab_fmt) {

@@ -257,6 +257,63 @@ cudaError_t launch_backward(const BackwardProblem& p, const LaunchCtx& c);
 cudaError_t launch_bf16_to_f16(const void* src, void* dst, int64_t n, int32_t* n_inexact,
                                const LaunchCtx& c);
 
+// ---- norm ------------------------------------------------------------------------
+constexpr int kNormMaxWidth = 16384;       // a row's values stay in registers
+constexpr int64_t kNormBackwardBlocks = 592;  // partial sums of the weight gradient
+struct NormProblem {
+  int64_t rows;
+  int d, bf16;  // type of x, residual, weight, sum_out and y
+  float eps;
+  const void* x;
+  const void* residual;  // or null
+  const void* weight;
+  void* sum_out;  // or null
+  void* y;        // or null
+  void* q;        // or null; then scale is not written
+  float* scale;   // [ceil(d / 128)][rows]
+  float* rstd;    // or null
+};
+cudaError_t launch_rmsnorm(const NormProblem& p, const LaunchCtx& c);
+struct NormBackwardProblem {
+  int64_t rows;
+  int d, bf16;
+  const void* r;
+  const void* weight;
+  const float* rstd;
+  const float* dy;
+  const float* dres;  // or null
+  float* dx;
+  float* dweight;     // or null
+  float* partial;     // [min(blocks, kNormBackwardBlocks)][d]
+};
+cudaError_t launch_rmsnorm_backward(const NormBackwardProblem& p, const LaunchCtx& c);
+
+// ---- 8-bit rows and products -----------------------------------------------------
+cudaError_t launch_quantize_rows(const void* x, int x_bf16, void* q, float* scale, int64_t rows,
+                                 int d, const LaunchCtx& c);
+cudaError_t launch_quantize_weights(const void* w, int w_bf16, void* q, float* scale,
+                                    int64_t groups, int n, int k, const LaunchCtx& c);
+// Permuted rows s < *n_kept of x_perm from token rows perm_src[s] / k of x.
+cudaError_t launch_gather_rows_fp8(const void* x, const float* xs, const int32_t* perm_src,
+                                   const int32_t* n_kept, void* x_perm, float* xs_perm, int64_t T,
+                                   int k, int d, const LaunchCtx& c);
+enum { kFp8OutBf16 = 0, kFp8OutF32 = 1, kFp8OutE4m3 = 2 };
+struct Fp8GemmProblem {
+  int64_t rows;  // of a and out (the row capacity of a grouped product)
+  int N, K;
+  int groups = 1;
+  const int32_t* offsets = nullptr;  // [groups + 1], or null: one group of all rows
+  const void* a;          // [rows, K] e4m3
+  const float* a_scale;   // [ceil(K / 128)][rows]
+  const void* b;          // [groups, N, K] e4m3
+  const float* b_scale;   // [groups][ceil(N / 128)][ceil(K / 128)]
+  int out_type;           // kFp8Out*
+  int act = 0;            // kFp8OutE4m3: 0 none, 1 ReLU, 2 GELU
+  void* out;              // [rows, N]
+  float* out_scale = nullptr;  // kFp8OutE4m3: [ceil(N / 128)][rows]
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c);
+
 // ---- host helpers shared by the entry points (moe_api.cu) ------------------------
 moe_status check_config_host(const moe_config* cfg);  // MOE_OK / INVALID_ARG / UNSUPPORTED
 int64_t capacity_host(const moe_config* cfg);         // C, or -1 for no limit
@@ -268,6 +325,9 @@ void set_last_launch_count(int32_t n);
 // out-of-range elements read as zero.
 bool make_tmap_2b(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                   uint32_t box_rows, int f16);
+// The same of 1-byte elements with a box of [box_rows, 128 columns].
+bool make_tmap_1b(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                  uint32_t box_rows);
 inline bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows) {
   return make_tmap_2b(map, base, rows, cols, box_rows, 0);
