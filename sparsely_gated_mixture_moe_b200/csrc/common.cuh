@@ -44,6 +44,19 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   return t;
 }
 
+// True in one lane of a converged warp, always the same one.  A loop that the whole warp
+// runs, with only its tcgen05 instructions behind this, keeps descriptors and addresses in
+// uniform registers, where those instructions take them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(on));
+  return on != 0;
+}
+
 // ------------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -261,6 +274,19 @@ __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The same, with the registers of a tmem_ld32 as operands: their uses cannot move above it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+
 // ------------------------------------------------- CTA pairs (clusters of two CTAs)
 //
 // The two CTAs of a cluster share one tensor-core product of M = 256 rows
@@ -296,6 +322,24 @@ __device__ __forceinline__ void cluster_sync_all() {
 // performed.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same where `on`, without a branch; CLUSTER: bar is a shared::cluster address.
+template <bool CLUSTER>
+__device__ __forceinline__ void mbar_arrive_relaxed_if(uint32_t bar, bool on) {
+  if (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(bar),
+        "r"(static_cast<int>(on))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(bar),
+        "r"(static_cast<int>(on))
+        : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
@@ -349,6 +393,14 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
                    bar)
                : "memory");
 }
+// Arrive once on the mbarrier at this shared::cta offset in both CTAs of the pair.
+__device__ __forceinline__ void tc_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
 // D[tmem] (+)= A * B^T over the pair: M = 256 (128 rows of A and D in each CTA), B split
 // by N between the CTAs; the descriptors name the same shared-memory offsets in both.
 __device__ __forceinline__ void tc_mma_pair_f16kind(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
@@ -357,6 +409,17 @@ __device__ __forceinline__ void tc_mma_pair_f16kind(uint32_t d_tmem, uint64_t ad
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with 8-bit inputs, K = 32.
+__device__ __forceinline__ void tc_mma_pair_f8kind(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                   uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

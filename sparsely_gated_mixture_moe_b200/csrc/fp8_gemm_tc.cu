@@ -13,13 +13,23 @@
 //               rows need) and B [BN x 128 B] per block into a ring of 128-byte-swizzled
 //               stages.
 //   warp 1      TMEM owner and MMA issuer: each block into the next of 512 / BN accumulators.
+//   warp 2      scales: the product of A's and B's scale for each row and 128 columns into
+//               shared memory beside the accumulator it belongs to, loaded some blocks ahead
+//               (by the epilogue itself, even as asynchronous copies, this cost it 350 clocks
+//               a block).  An accumulator is full when both its products and scales are.
+//   warp 3      idle: a warpgroup gives its registers up as a whole.
 //   others      four epilogue warps per 128 columns: a thread owns a row and 128 columns, that
 //               is one scale of A and one of B per block, and the whole scale block of an
 //               e4m3 output, whose maximum it takes in registers.
 // A row past the tile's last may hold anything (another group's row, an earlier stage's
 // bytes): it only reaches its own output row, which is not stored.  Columns past K and rows
 // past the last group read as zero.
-// No cross-CTA waits; every mbarrier wait is bounded and an expired wait sets kErrTimeout,
+// Large groups run on CTA pairs (clusters of two, tcgen05 cta_group::2): a tile has 256 rows,
+// each CTA loads its 128 rows of A and half of B, one thread of rank 0 issues the MMAs for both,
+// and each CTA's epilogue reads its own rows from its own TMEM.  Per SM and block that is 32 KB
+// written to and read from shared memory instead of 48: at 128 bytes a clock the single form's
+// 96 KB take 768 clocks, more than the tensor cores' 512.
+// No waits on other clusters; every mbarrier wait is bounded and an expired wait sets kErrTimeout,
 // drains this CTA's in-flight copies and MMAs and frees TMEM.
 #include "fp8.cuh"
 #include "internal.h"
@@ -34,17 +44,23 @@ constexpr int A_BYTES = BM * BK;
 constexpr int RING_BYTES = 192 * 1024;
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
+constexpr int CW = 128;    // columns of an epilogue thread: a scale block
+constexpr int SCALE_FLOATS = 1024;  // 2 BUFS slots of BN
 constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + 256 /*barriers, flags*/ +
-                           4 * (MAX_GROUPS + 1 + 40);
+                           SCALE_FLOATS * 4 /*scales*/ + 4 * (MAX_GROUPS + 1 + 40);
 
-template <int BN>
+// BN columns a tile; PAIR: two CTAs share a tile of 256 rows.
+template <int BN, bool PAIR>
 struct Cfg {
-  static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
-  static constexpr int STAGES = RING_BYTES / STAGE_BYTES;  // 4 (BN = 256) or 6
-  static constexpr int BUFS = TMEM_COLS / BN;              // 2 or 4
-  static constexpr int EPI_WARPS = BN / 32;                // 8 or 4
-  static constexpr int THREADS = 64 + EPI_WARPS * 32;
+  static constexpr int TBM = PAIR ? 2 * BM : BM;           // rows of a tile
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
+  static constexpr int STAGES = RING_BYTES / STAGE_BYTES;  // 6 (pair, BN = 128) or 4
+  static constexpr int BUFS = BN == 256 ? 2 : 3;           // accumulators
+  static constexpr int EPI_WARPS = BN / CW * 4;            // 8 or 4
+  static constexpr int THREADS = 128 + EPI_WARPS * 32;
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
+  static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS && STAGES % BUFS == 0, "whole turns of the accumulators a ring");
 };
 
 struct Args {
@@ -66,14 +82,14 @@ struct Tile {
   int valid;
 };
 
-__device__ __forceinline__ Tile decode_tile(int L, const int* tp, const Args& a) {
+__device__ __forceinline__ Tile decode_tile(int L, const int* tp, const Args& a, int bm) {
   Tile t;
   if (a.offsets == nullptr) {
     t.g = 0;
     const int mt = L / a.n_tiles;
     t.nt = L - mt * a.n_tiles;
-    t.row0 = static_cast<int64_t>(mt) * BM;
-    t.valid = static_cast<int>(min(static_cast<int64_t>(BM), a.rows - t.row0));
+    t.row0 = static_cast<int64_t>(mt) * bm;
+    t.valid = static_cast<int>(min(static_cast<int64_t>(bm), a.rows - t.row0));
     return t;
   }
   int lo = 0, hi = a.groups - 1;  // the largest g with tp[g] * n_tiles <= L
@@ -86,25 +102,26 @@ __device__ __forceinline__ Tile decode_tile(int L, const int* tp, const Args& a)
   const int mt = local / a.n_tiles;
   t.nt = local - mt * a.n_tiles;
   const int r0 = __ldg(a.offsets + lo), r1 = __ldg(a.offsets + lo + 1);
-  t.row0 = r0 + mt * BM;
-  t.valid = min(BM, r1 - static_cast<int>(t.row0));
+  t.row0 = r0 + mt * bm;
+  t.valid = min(bm, r1 - static_cast<int>(t.row0));
   return t;
 }
 
+// Boxes of A that cover a CTA's rows of a tile.
+__device__ __forceinline__ int a_boxes(int valid) {
+  return (max(0, min(valid, BM)) + A_BOX - 1) / A_BOX;
+}
+
 // Stores of one row's finished sums: `n` columns (a multiple of 8, at most 128) from dst on.
-__device__ __forceinline__ void store_bf16(void* out, int64_t at, const uint64_t (&acc)[64], int n,
+__device__ __forceinline__ void store_bf16(void* out, int64_t at, const float (&acc)[CW], int n,
                                            int vec32) {
   uint16_t* dst = static_cast<uint16_t*>(out) + at;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < CW / 16; ++c) {
     if (c * 16 >= n) break;
     uint32_t p[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float lo, hi;
-      f2_unpack(acc[c * 8 + j], lo, hi);
-      p[j] = pack_bf16x2(lo, hi);
-    }
+    for (int j = 0; j < 8; ++j) p[j] = pack_bf16x2(acc[c * 16 + 2 * j], acc[c * 16 + 2 * j + 1]);
     if (vec32 && c * 16 + 16 <= n) {
       st_global_v8(dst + c * 16, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]);
     } else {
@@ -114,15 +131,15 @@ __device__ __forceinline__ void store_bf16(void* out, int64_t at, const uint64_t
   }
 }
 
-__device__ __forceinline__ void store_f32(void* out, int64_t at, const uint64_t (&acc)[64], int n,
+__device__ __forceinline__ void store_f32(void* out, int64_t at, const float (&acc)[CW], int n,
                                           int vec32) {
   float* dst = static_cast<float*>(out) + at;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < CW / 8; ++c) {
     if (c * 8 >= n) break;
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f2_unpack(acc[c * 4 + j], v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 8; ++j) v[j] = acc[c * 8 + j];
     if (vec32) {
       uint32_t u[8];
 #pragma unroll
@@ -138,13 +155,12 @@ __device__ __forceinline__ void store_f32(void* out, int64_t at, const uint64_t 
 // values are fp32 sums: a product with the rounded reciprocal of the scale errs by at most
 // 2^-23 of the quotient, against e4m3's half step of 2^-4.
 template <int ACT>
-__device__ __forceinline__ void store_e4m3(void* out, int64_t at, float* scale,
-                                           uint64_t (&acc)[64], int n) {
+__device__ __forceinline__ void store_e4m3(void* out, int64_t at, float* scale, float (&acc)[CW],
+                                           int n) {
   float m = kAmaxFloor;
 #pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    float lo, hi;
-    f2_unpack(acc[j], lo, hi);
+  for (int j = 0; j < CW / 2; ++j) {
+    float &lo = acc[2 * j], &hi = acc[2 * j + 1];
     if (2 * j >= n) {
       lo = hi = 0.0f;
     } else if (ACT == 1) {
@@ -155,31 +171,27 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, float* scale,
       gelu2_as7126(lo, hi, lo, hi);
     }
     m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
-    acc[j] = f2_pack(lo, hi);
   }
-  const uint64_t inv = f2_splat(kE4m3Max / m);
+  const float inv = kE4m3Max / m;
   uint8_t* dst = static_cast<uint8_t*>(out) + at;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < CW / 16; ++c) {
     if (c * 16 >= n) break;
     uint32_t p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v0, v1, v2, v3;
-      f2_unpack(f2_mul(acc[c * 8 + 2 * j], inv), v0, v1);
-      f2_unpack(f2_mul(acc[c * 8 + 2 * j + 1], inv), v2, v3);
-      p[j] = pack_e4m3x4(v0, v1, v2, v3);
-    }
+    for (int j = 0; j < 4; ++j)
+      p[j] = pack_e4m3x4(acc[c * 16 + 4 * j] * inv, acc[c * 16 + 4 * j + 1] * inv,
+                         acc[c * 16 + 4 * j + 2] * inv, acc[c * 16 + 4 * j + 3] * inv);
     *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(p[0], p[1], p[2], p[3]);
   }
   *scale = block_scale(m);
 }
 
-template <int BN, int OUT>
-__global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
+template <int BN, int OUT, bool PAIR>
+__global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     fp8_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB, const Args a) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -192,9 +204,14 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   const uint32_t drain = smem_u32(bars + 2 * C::STAGES + 2 * C::BUFS);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * C::BUFS + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* scratch = reinterpret_cast<int*>(smem + RING_BYTES + 256);
+  float* scales = reinterpret_cast<float*>(smem + RING_BYTES + 256);  // [2 BUFS][BN / 128][128 rows]
+  int* scratch = reinterpret_cast<int*>(scales + SCALE_FLOATS);
   int* tp = scratch + 40;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+  const int step = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -202,8 +219,8 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < C::BUFS; ++b) {
-      mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, C::EPI_WARPS);
+      mbar_init(tfull0 + 8 * b, 2);  // the products and their scales
+      mbar_init(tempty0 + 8 * b, (PAIR ? 2 : 1) * C::EPI_WARPS);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -212,46 +229,65 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   grid_dep_wait();  // the operands come from the previous kernels on the stream
   grid_dep_launch();
   int tiles;
   if (a.offsets != nullptr) {
-    const bool ok = block_tile_prefix(a.offsets, a.groups, a.rows, BM, tp, scratch);
+    const bool ok = block_tile_prefix(a.offsets, a.groups, a.rows, C::TBM, tp, scratch);
     if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_error(a.err, kErrOffsets);
     tiles = ok ? tp[a.groups] * a.n_tiles : 0;
   } else {
-    tiles = static_cast<int>((a.rows + BM - 1) / BM) * a.n_tiles;
+    tiles = static_cast<int>((a.rows + C::TBM - 1) / C::TBM) * a.n_tiles;
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-
-  if (warp == 0) {
-    if (lane == 0) {
+  // BN = 256: 12 warps start with 168 registers a thread; the first warpgroup's go to the
+  // epilogue's sums (136 + 2 * 184 = 3 * 168: the scale warp's loads in flight)
+  if (warp < 4) {
+    if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
+    if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------ TMA producer
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool aborted = false;
-      for (int L = blockIdx.x; L < tiles && !aborted; L += gridDim.x) {
-        const Tile t = decode_tile(L, tp, a);
-        const int brow = t.g * a.N + t.nt * BN;
-        const int boxes = (t.valid + A_BOX - 1) / A_BOX;
-        const uint32_t tx = static_cast<uint32_t>(boxes * A_BOX * BK + BN * BK);
+      for (int L = first; L < tiles && !aborted; L += step) {
+        const Tile t = decode_tile(L, tp, a, C::TBM);
+        const int brow = t.g * a.N + t.nt * BN + rank * C::B_ROWS;
+        const int arow = static_cast<int>(t.row0) + rank * BM;
+        const int boxes = a_boxes(t.valid - rank * BM);
+        // a pair's copies all complete on the barrier of rank 0
+        const uint32_t tx = static_cast<uint32_t>(
+            (PAIR ? a_boxes(t.valid) + a_boxes(t.valid - BM) : boxes) * A_BOX * BK + BN * BK);
         for (int kb = 0; kb < a.kblocks; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, s_abort)) {
             aborted = true;
             break;
           }
           const uint32_t st = smem_u32(ring + stage * C::STAGE_BYTES);
-          const uint32_t fb = full0 + 8 * stage;
-          mbar_arrive_expect_tx(fb, tx);
-          tma_load_2d(st + A_BYTES, &tmB, fb, kb * BK, brow);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(st + i * A_BOX * BK, &tmA, fb, kb * BK, static_cast<int>(t.row0) + i * A_BOX);
+          if constexpr (PAIR) {
+            const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+            tma_load_2d_pair(st + A_BYTES, &tmB, fb, kb * BK, brow);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d_pair(st + i * A_BOX * BK, &tmA, fb, kb * BK, arow + i * A_BOX);
+          } else {
+            const uint32_t fb = full0 + 8 * stage;
+            mbar_arrive_expect_tx(fb, tx);
+            tma_load_2d(st + A_BYTES, &tmB, fb, kb * BK, brow);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(st + i * A_BOX * BK, &tmA, fb, kb * BK, arow + i * A_BOX);
+          }
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           if (++stage == C::STAGES) {
@@ -263,98 +299,189 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
       if (aborted) {
         set_error(a.err, kErrTimeout);
         *s_abort = 1;
-        // let every copy this thread started land before the CTA releases its smem
-        for (int s = 0; s < C::STAGES; ++s)
-          if (armed & (1u << s)) mbar_wait(full0 + 8 * s, (armed_par >> s) & 1, nullptr, kDrainLimitNs);
+        // let every copy this thread started land before the CTA releases its smem (a pair's
+        // second CTA cannot watch rank 0's barrier: it waits out a fixed drain time)
+        if (rank == 0) {
+          for (int s = 0; s < C::STAGES; ++s)
+            if (armed & (1u << s)) mbar_wait(full0 + 8 * s, (armed_par >> s) & 1, nullptr, kDrainLimitNs);
+        } else {
+          const unsigned long long t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < kDrainLimitNs / 4) __nanosleep(1000);
+        }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == 1 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_f32acc(BM, BN, kFmtE4M3);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+      // This one thread's instructions bound the kernel before they were cut to the bone (760
+      // clocks a block, of which the tensor cores need 512): the loop runs over all blocks of
+      // all of the CTA's tiles, one turn of the ring at a time, so that every stage, accumulator
+      // and its parity is a constant.
+      constexpr uint32_t idesc = idesc_f32acc(C::TBM, BN, kFmtE4M3);
+      const int64_t blocks = first < tiles ? static_cast<int64_t>((tiles - first + step - 1) / step) * a.kblocks : 0;
+      const uint64_t desc0 = sdesc_k128(smem_u32(ring));
+      uint32_t phase = 0;
       bool aborted = false;
-      for (int L = blockIdx.x; L < tiles && !aborted; L += gridDim.x) {
-        for (int kb = 0; kb < a.kblocks; ++kb) {
-          if (!mbar_wait(tempty0 + 8 * buf, buf_phase ^ 1, s_abort) ||
-              !mbar_wait(full0 + 8 * stage, phase, s_abort)) {
+      for (int64_t i = 0; i < blocks && !aborted; i += C::STAGES) {
+        const int left = static_cast<int>(min(blocks - i, static_cast<int64_t>(C::STAGES)));
+#pragma unroll
+        for (int st = 0; st < C::STAGES; ++st) {
+          constexpr int kA = A_BYTES >> 4;
+          const int buf = st % C::BUFS;
+          const uint32_t turn = st / C::BUFS % 2;  // an odd number of turns: the parity alternates
+          if (st >= left) break;
+          if (!mbar_wait(full0 + 8 * st, phase, s_abort) ||
+              !mbar_wait(tempty0 + 8 * buf, (turn ^ (C::STAGES / C::BUFS % 2 ? phase : 0)) ^ 1, s_abort)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(ring + stage * C::STAGE_BYTES);
-          const uint32_t b0 = a0 + A_BYTES;
+          // descriptors differ in their start address alone (its 14 bits do not overflow: the
+          // ring ends below 256 KB)
+          const uint64_t da = desc0 + st * (C::STAGE_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            tc_mma_f8kind(tmem_base + buf * BN, sdesc_k128(a0 + kk * 32), sdesc_k128(b0 + kk * 32),
-                          idesc, kk != 0 ? 1u : 0u);
-          tc_commit(empty0 + 8 * stage);
-          tc_commit(tfull0 + 8 * buf);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
+            for (int kk = 0; kk < BK / 32; ++kk) {
+              if constexpr (PAIR)
+                tc_mma_pair_f8kind(tmem_base + buf * BN, da + kk * 2, da + kA + kk * 2, idesc, kk != 0 ? 1u : 0u);
+              else
+                tc_mma_f8kind(tmem_base + buf * BN, da + kk * 2, da + kA + kk * 2, idesc, kk != 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              tc_commit_both(tfull0 + 8 * buf);
+              tc_commit_both(empty0 + 8 * st);
+            } else {
+              tc_commit(tfull0 + 8 * buf);
+              tc_commit(empty0 + 8 * st);
+            }
           }
-          if (++buf == C::BUFS) {
-            buf = 0;
-            buf_phase ^= 1;
-          }
+          __syncwarp();
         }
+        phase ^= 1;
       }
       if (aborted) {
         set_error(a.err, kErrTimeout);
         *s_abort = 1;
         // wait for the MMAs already issued before TMEM is freed
-        tc_commit(drain);
+        if (elect_one()) {
+          if constexpr (PAIR) tc_commit_pair(mapa_shared(drain, 0));
+          else tc_commit(drain);
+        }
         mbar_wait(drain, 0, nullptr, kDrainLimitNs);
       }
     }
+    if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      // GROUP blocks at a time: the next group's loads are in flight while this one's wait
+      // for their accumulators.
+      constexpr int GROUP = 4, HALVES = BN / CW;
+      struct Ahead {
+        float a[GROUP][4], b[GROUP][HALVES];
+      };
+      auto load = [&](Ahead& v, const Tile& t, int kb0) {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+          const int kb = min(kb0 + i, a.kblocks - 1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v.a[i][j] = __ldg(a.a_scale + static_cast<int64_t>(kb) * a.rows + t.row0 +
+                              min(rank * BM + lane + 32 * j, t.valid - 1));
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const int nb = min(t.nt * HALVES + h, a.nblocks - 1);
+            v.b[i][h] = __ldg(a.b_scale + (static_cast<int64_t>(t.g) * a.nblocks + nb) * a.kblocks + kb);
+          }
+        }
+      };
+      // A slot may be written once the epilogue has read what it held 2 BUFS blocks before:
+      // the products of BUFS blocks before would not be complete, had their accumulator not
+      // been free of that.
+      int buf = 0, slot = 0;
+      uint32_t buf_phase = 1;  // a barrier's first turn: nothing to wait for
+      bool aborted = false;
+      Ahead next;
+      if (first < tiles) load(next, decode_tile(first, tp, a, C::TBM), 0);
+      for (int L = first; L < tiles && !aborted; L += step) {
+        const Tile t = decode_tile(L, tp, a, C::TBM);
+        for (int kb0 = 0; kb0 < a.kblocks && !aborted; kb0 += GROUP) {
+          const Ahead v = next;
+          if (kb0 + GROUP < a.kblocks) load(next, t, kb0 + GROUP);
+          else if (L + step < tiles) load(next, decode_tile(L + step, tp, a, C::TBM), 0);
+#pragma unroll
+          for (int i = 0; i < GROUP; ++i) {
+            if (kb0 + i >= a.kblocks) break;
+            if (!mbar_wait(tfull0 + 8 * buf, buf_phase, s_abort)) {
+              aborted = true;
+              break;
+            }
+            float* to = scales + slot * BN + lane;
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) to[h * CW + 32 * j] = v.a[i][j] * v.b[i][h];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tfull0 + 8 * buf);
+            if (++slot == 2 * C::BUFS) slot = 0;
+            if (++buf == C::BUFS) {
+              buf = 0;
+              buf_phase ^= 1;
+            }
+          }
+        }
+      }
+      if (aborted) {
+        if (lane == 0) set_error(a.err, kErrTimeout);
+        *s_abort = 1;
+      }
+    }
   } else {
+    if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;       // TMEM lane quarter this warp may read
-    const int half = (warp - 2) >> 2;   // which 128 columns of the tile
+    const int cg = (warp - 4) >> 2;     // which 128 columns of the tile
     const int r = quarter * 32 + lane;
-    int buf = 0;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + cg * CW;
+    const float* my_scale = scales + cg * CW + r;
+    const uint32_t free0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
+    int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool aborted = false;
-    for (int L = blockIdx.x; L < tiles && !aborted; L += gridDim.x) {
-      const Tile t = decode_tile(L, tp, a);
-      const bool row_ok = r < t.valid;
-      const bool warp_ok = quarter * 32 < t.valid;
-      const int64_t row = t.row0 + (row_ok ? r : 0);
-      const int nb = min(t.nt * (BN / 128) + half, a.nblocks - 1);
-      const float* as = a.a_scale + row;
-      const float* bs = a.b_scale + (static_cast<int64_t>(t.g) * a.nblocks + nb) * a.kblocks;
-      uint64_t acc[64];
+    for (int L = first; L < tiles && !aborted; L += step) {
+      const Tile t = decode_tile(L, tp, a, C::TBM);
+      const int valid = t.valid - rank * BM;
+      const bool row_ok = r < valid, warp_ok = quarter * 32 < valid;
+      float acc[CW];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-      float s_next = __ldg(as) * __ldg(bs);
+      for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
       for (int kb = 0; kb < a.kblocks; ++kb) {
-        const uint64_t s = f2_splat(s_next);
-        if (kb + 1 < a.kblocks)
-          s_next = __ldg(as + static_cast<int64_t>(kb + 1) * a.rows) * __ldg(bs + kb + 1);
         if (!mbar_wait(tfull0 + 8 * buf, buf_phase, s_abort)) {
           aborted = true;
           break;
         }
+        const uint32_t free_bar = free0 + 8 * buf;
         if (warp_ok) {
           tc_fence_after();
-          const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + half * 128;
+          const float s = my_scale[slot * BN];
+          const uint32_t tb = lanes + buf * BN;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < CW / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(tb + c * 32, v);
-            tmem_ld_wait();
+            tmem_ld_wait32(v);
+            // the warp's last TMEM read is complete (and its scale read: s is used below):
+            // the accumulator is free before the last sums.  Relaxed, since nothing else is
+            // handed on.
+            if (c == CW / 32 - 1) {
+              tc_fence_before();
+              mbar_arrive_relaxed_if<PAIR>(free_bar, lane == 0);
+            }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[c * 16 + j] = f2_fma(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                                       s, acc[c * 16 + j]);
+            for (int j = 0; j < 32; ++j)
+              acc[c * 32 + j] = fmaf(__uint_as_float(v[j]), s, acc[c * 32 + j]);
           }
-          tc_fence_before();
+        } else {
+          mbar_arrive_relaxed_if<PAIR>(free_bar, lane == 0);
         }
-        __syncwarp();
-        // relaxed: the TMEM reads are complete (tcgen05.wait::ld) and nothing else is handed on
-        if (lane == 0) mbar_arrive_relaxed(tempty0 + 8 * buf);
+        if (++slot == 2 * C::BUFS) slot = 0;
         if (++buf == C::BUFS) {
           buf = 0;
           buf_phase ^= 1;
@@ -365,16 +492,16 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         *s_abort = 1;
         break;
       }
-      const int col = t.nt * BN + half * 128;
+      const int col = t.nt * BN + cg * CW;
       if (row_ok && col < a.N) {
-        const int n = min(128, a.N - col);
-        const int64_t at = row * a.N + col;
+        const int n = min(CW, a.N - col);
+        const int64_t row = t.row0 + rank * BM + r, at = row * a.N + col;
         if (OUT == kFp8OutBf16) {
           store_bf16(a.out, at, acc, n, a.vec32);
         } else if (OUT == kFp8OutF32) {
           store_f32(a.out, at, acc, n, a.vec32);
         } else {
-          float* sc = a.out_scale + static_cast<int64_t>(nb) * a.rows + row;
+          float* sc = a.out_scale + static_cast<int64_t>(col / kScaleBlock) * a.rows + row;
           if (a.act == 2) store_e4m3<2>(a.out, at, sc, acc, n);
           else if (a.act == 1) store_e4m3<1>(a.out, at, sc, acc, n);
           else store_e4m3<0>(a.out, at, sc, acc, n);
@@ -386,35 +513,51 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // a pair's CTAs leave together: rank 0's MMAs read the other CTA's shared memory and the
+  // other CTA's epilogue arrives on rank 0's barriers
+  if constexpr (PAIR) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else tmem_dealloc(tmem_base, TMEM_COLS);
+  }
 }
 
 }  // namespace f8
 
-template <int BN, int OUT>
+// Groups of at least this many rows on average run on CTA pairs.
+constexpr int64_t kFp8PairMinRows = 256;
+
+template <int BN, int OUT, bool PAIR>
 static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const LaunchCtx& c) {
+  using C = f8::Cfg<BN, PAIR>;
+  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, PAIR>;
   CUtensorMap tmA, tmB;
   if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, f8::A_BOX) ||
-      !make_tmap_1b(&tmB, p.b, static_cast<uint64_t>(p.groups) * p.N, p.K, BN))
+      !make_tmap_1b(&tmB, p.b, static_cast<uint64_t>(p.groups) * p.N, p.K, C::B_ROWS))
     return cudaErrorInvalidValue;
   a.n_tiles = (p.N + BN - 1) / BN;
-  // upper bound of the tile count: sum over groups of ceil(rows / 128)
+  // upper bound of the tile count: sum over groups of ceil(rows / TBM)
   const int64_t active = p.rows < p.groups ? p.rows : p.groups;
-  const int64_t tiles = (p.offsets == nullptr ? (p.rows + f8::BM - 1) / f8::BM
-                                              : p.rows / f8::BM + active) * a.n_tiles;
-  const int grid = static_cast<int>(tiles < c.num_sms ? tiles : c.num_sms);
-  cudaError_t e = ensure_smem_limit(f8::fp8_gemm_tc_kernel<BN, OUT>, f8::SMEM_BYTES);
+  const int64_t tiles = (p.offsets == nullptr ? (p.rows + C::TBM - 1) / C::TBM
+                                              : p.rows / C::TBM + active) * a.n_tiles;
+  cudaError_t e = ensure_smem_limit(kernel, f8::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return launch_kernel(f8::fp8_gemm_tc_kernel<BN, OUT>, dim3(grid), dim3(f8::Cfg<BN>::THREADS),
-                       f8::SMEM_BYTES, c, tmA, tmB, a);
+  if (PAIR) {
+    const int64_t cap = max_active_pairs(kernel, C::THREADS, f8::SMEM_BYTES, c);
+    return launch_kernel_pairs(kernel, dim3(static_cast<unsigned>(2 * (tiles < cap ? tiles : cap))),
+                               dim3(C::THREADS), f8::SMEM_BYTES, c, tmA, tmB, a);
+  }
+  const int64_t grid = tiles < c.num_sms ? tiles : c.num_sms;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), f8::SMEM_BYTES,
+                       c, tmA, tmB, a);
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 static cudaError_t launch_out(const Fp8GemmProblem& p, const f8::Args& a, const LaunchCtx& c) {
-  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16>(p, a, c);
-  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32>(p, a, c);
-  return launch_tiles<BN, kFp8OutE4m3>(p, a, c);
+  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, PAIR>(p, a, c);
+  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, PAIR>(p, a, c);
+  return launch_tiles<BN, kFp8OutE4m3, PAIR>(p, a, c);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
@@ -435,7 +578,9 @@ cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
   const int64_t row_bytes = static_cast<int64_t>(p.N) * (p.out_type == kFp8OutF32 ? 4 : 2);
   a.vec32 = row_bytes % 32 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
   a.err = c.err;
-  return p.N > 128 ? launch_out<256>(p, a, c) : launch_out<128>(p, a, c);
+  if (p.N <= 128) return launch_out<128, false>(p, a, c);
+  if (p.rows >= kFp8PairMinRows * p.groups) return launch_out<256, true>(p, a, c);
+  return launch_out<256, false>(p, a, c);
 }
 
 }  // namespace moe

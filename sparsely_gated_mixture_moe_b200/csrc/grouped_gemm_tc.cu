@@ -621,36 +621,6 @@ static int pick_bn(int N) {
 // tiles); from 512 on that share is small.
 constexpr int64_t kPairMinRowsPerExpert = 512;
 
-// Clusters of two CTAs of grouped_gemm_tc_kernel<true> that fit on the device at once (a
-// persistent grid larger than that would serialise), looked up once per context.
-static int max_active_pairs(const LaunchCtx& c) {
-  static std::mutex mu;
-  static std::map<unsigned long long, int> cache;
-  unsigned long long ctx = 0;
-  if (current_context_id(&ctx) != cudaSuccess) return c.num_sms / 2;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(ctx);
-  if (it != cache.end()) return it->second;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (c.num_sms / 2));
-  cfg.blockDim = dim3(gg::THREADS);
-  cfg.dynamicSmemBytes = gg::SMEM_BYTES;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gg::grouped_gemm_tc_kernel<true>, &cfg) != cudaSuccess ||
-      n <= 0)
-    n = c.num_sms / 2;
-  if (n > c.num_sms / 2) n = c.num_sms / 2;
-  cache[ctx] = n;
-  return n;
-}
-
 // A: the permuted rows [rows_cap, K], or with gather_src the token rows [a_rows, K] that
 // permuted row s reads at row gather_src[s] / gather_k.
 static cudaError_t launch_one(const void* A, int64_t rows_cap, int K, const void* B, int E, int N,
@@ -703,7 +673,7 @@ static cudaError_t launch_one(const void* A, int64_t rows_cap, int K, const void
   if (pair) {
     cudaError_t e = ensure_smem_limit(gg::grouped_gemm_tc_kernel<true>, gg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const int64_t pairs_cap = max_active_pairs(c);
+    const int64_t pairs_cap = max_active_pairs(gg::grouped_gemm_tc_kernel<true>, gg::THREADS, gg::SMEM_BYTES, c);
     const int pairs = static_cast<int>(max_tiles < pairs_cap ? max_tiles : pairs_cap);
     if (pairs <= 0) return cudaSuccess;
     return launch_kernel_pairs(gg::grouped_gemm_tc_kernel<true>, dim3(2 * pairs), dim3(gg::THREADS),

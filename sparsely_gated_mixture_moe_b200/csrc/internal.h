@@ -96,6 +96,37 @@ cudaError_t launch_kernel_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block,
   return e;
 }
 
+// Clusters of two CTAs of a kernel that fit on the device at once (a persistent grid larger
+// than that would serialise), looked up once per context and kernel.  Its shared-memory limit
+// has been raised before.
+template <typename... KArgs>
+int max_active_pairs(void (*kernel)(KArgs...), int threads, int smem, const LaunchCtx& c) {
+  static std::mutex mu;
+  static std::map<std::pair<unsigned long long, const void*>, int> cache;
+  unsigned long long ctx = 0;
+  if (current_context_id(&ctx) != cudaSuccess) return c.num_sms / 2;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(ctx, reinterpret_cast<const void*>(kernel));
+  const auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (c.num_sms / 2));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) n = c.num_sms / 2;
+  if (n > c.num_sms / 2) n = c.num_sms / 2;
+  cache[key] = n;
+  return n;
+}
+
 // ---- route -----------------------------------------------------------------------
 struct RouteProblem {
   int64_t T;
