@@ -39,15 +39,13 @@ namespace f8 {
 
 constexpr int BM = 128;
 constexpr int BK = 128;  // bytes of a k-block's rows: one scale block of the contraction
-constexpr int A_BOX = 32;
 constexpr int A_BYTES = BM * BK;
-constexpr int RING_BYTES = 192 * 1024;
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr int CW = 128;    // columns of an epilogue thread: a scale block
-constexpr int SCALE_FLOATS = 1024;  // 2 BUFS slots of BN
-constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + 256 /*barriers, flags*/ +
-                           SCALE_FLOATS * 4 /*scales*/ + 4 * (MAX_GROUPS + 1 + 40);
+constexpr int SCALE_FLOATS = 1024;  // slots of 2 BUFS blocks
+constexpr int BUFS = 2;             // accumulators
+constexpr int STAGED = 32 * 256;    // bytes of output a warp stages: 32 rows of 256
 
 // BN columns a tile; PAIR: two CTAs share a tile of 256 rows.
 template <int BN, bool PAIR>
@@ -55,12 +53,18 @@ struct Cfg {
   static constexpr int TBM = PAIR ? 2 * BM : BM;           // rows of a tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
-  static constexpr int STAGES = RING_BYTES / STAGE_BYTES;  // 6 (pair, BN = 128) or 4
-  static constexpr int BUFS = BN == 256 ? 2 : 3;           // accumulators
+  static constexpr int STAGES = !PAIR && BN == 256 ? 3 : 4;
+  static constexpr int TURN = STAGES % BUFS == 0 ? STAGES : STAGES * BUFS;  // of stages and accumulators
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 KB, or 144 (single, BN = 256)
+  // rows of A in one copy: a small group's tile needs few
+  static constexpr int A_BOX = PAIR ? BM : 32;
   static constexpr int EPI_WARPS = BN / CW * 4;            // 8 or 4
   static constexpr int THREADS = 128 + EPI_WARPS * 32;
+  static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + EPI_WARPS * STAGED +
+                                    256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
+                                    4 * (MAX_GROUPS + 1 + 40);
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
-  static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS && STAGES % BUFS == 0, "whole turns of the accumulators a ring");
+  static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS, "scales and accumulators fit");
 };
 
 struct Args {
@@ -71,7 +75,7 @@ struct Args {
   const float* b_scale;
   void* out;
   float* out_scale;
-  int act;
+  int act;    // kFp8OutE4m3: 1 ReLU, 2 GELU
   int vec32;  // output rows start on 32-byte boundaries
   int* err;
 };
@@ -108,8 +112,85 @@ __device__ __forceinline__ Tile decode_tile(int L, const int* tp, const Args& a,
 }
 
 // Boxes of A that cover a CTA's rows of a tile.
+template <int A_BOX>
 __device__ __forceinline__ int a_boxes(int valid) {
   return (max(0, min(valid, BM)) + A_BOX - 1) / A_BOX;
+}
+
+// 2-D tiled bulk tensor store shared -> global (box as in the map, 128-byte swizzled rows of
+// 128 bytes; columns past the tensor's are not written), one commit group of the thread.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until this thread's stores have read shared memory, or are complete.
+__device__ __forceinline__ void bulk_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Makes this thread's writes to shared memory visible to bulk copies.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void stage16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Outputs of a warp all of whose 32 rows are stored go by way of shared memory: each thread
+// writes its row, 128 bytes to a box, in the swizzle of the output's tensor map (16-byte piece i
+// of row r at i ^ (r mod 8): 8 lanes fall on different banks), and one lane stores the
+// boxes, which the sums of the next tile do not wait for.  Stored directly, each row costs an
+// access of its own for every 32 bytes: 3,850 clocks a tile of 128 x 256.
+// `to`: the warp's staging place, 1024-byte aligned, boxes of 4 KB; the last store's reads end
+// before it is written again.
+__device__ __forceinline__ uint32_t staged_piece(uint32_t to, int lane, int box, int i) {
+  return to + box * 4096 + lane * 128 + ((i ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ void staging_begin(int lane) {
+  if (lane == 0) bulk_store_wait_read();
+  __syncwarp();
+}
+// Boxes of `width` columns from x on, as many as start before column N.
+__device__ __forceinline__ void staging_end(const CUtensorMap* map, uint32_t to, int lane, int boxes,
+                                            int width, int x, int y, int N) {
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    for (int b = 0; b < boxes; ++b)
+      if (x + b * width < N) tma_store_2d(map, to + b * 4096, x + b * width, y);
+    bulk_store_commit();
+  }
+}
+__device__ __forceinline__ void put_bf16(const CUtensorMap* map, uint32_t to, int lane,
+                                         const float (&acc)[CW], int x, int y, int N) {
+  staging_begin(lane);
+#pragma unroll
+  for (int c = 0; c < CW / 8; ++c)
+    stage16(staged_piece(to, lane, c / 8, c % 8), pack_bf16x2(acc[c * 8], acc[c * 8 + 1]),
+            pack_bf16x2(acc[c * 8 + 2], acc[c * 8 + 3]), pack_bf16x2(acc[c * 8 + 4], acc[c * 8 + 5]),
+            pack_bf16x2(acc[c * 8 + 6], acc[c * 8 + 7]));
+  staging_end(map, to, lane, 2, 64, x, y, N);
+}
+__device__ __forceinline__ void put_f32(const CUtensorMap* map, uint32_t to, int lane,
+                                        const float (&acc)[CW], int x, int y, int N) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    staging_begin(lane);
+#pragma unroll
+    for (int c = 0; c < CW / 8; ++c)
+      stage16(staged_piece(to, lane, c / 8, c % 8), __float_as_uint(acc[h * 64 + c * 4]),
+              __float_as_uint(acc[h * 64 + c * 4 + 1]), __float_as_uint(acc[h * 64 + c * 4 + 2]),
+              __float_as_uint(acc[h * 64 + c * 4 + 3]));
+    staging_end(map, to, lane, 2, 32, x + h * 64, y, N);
+  }
 }
 
 // Stores of one row's finished sums: `n` columns (a multiple of 8, at most 128) from dst on.
@@ -151,12 +232,9 @@ __device__ __forceinline__ void store_f32(void* out, int64_t at, const float (&a
   }
 }
 
-// Activation, then the row's scale block as e4m3 and its scale.  n is a multiple of 16.  The
-// values are fp32 sums: a product with the rounded reciprocal of the scale errs by at most
-// 2^-23 of the quotient, against e4m3's half step of 2^-4.
+// Activation of the row's 128 columns (zero from column n on) and the largest magnitude.
 template <int ACT>
-__device__ __forceinline__ void store_e4m3(void* out, int64_t at, float* scale, float (&acc)[CW],
-                                           int n) {
+__device__ __forceinline__ float activate(float (&acc)[CW], int n) {
   float m = kAmaxFloor;
 #pragma unroll
   for (int j = 0; j < CW / 2; ++j) {
@@ -172,39 +250,61 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, float* scale, 
     }
     m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
   }
-  const float inv = kE4m3Max / m;
+  return m;
+}
+
+// 16 values of the row's scale block as e4m3.  They are fp32 sums: a product with the rounded
+// reciprocal of the scale errs by at most 2^-23 of the quotient, against e4m3's half step of
+// 2^-4.
+__device__ __forceinline__ uint4 pack16_e4m3(const float (&acc)[CW], int c, float inv) {
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    p[j] = pack_e4m3x4(acc[c * 16 + 4 * j] * inv, acc[c * 16 + 4 * j + 1] * inv,
+                       acc[c * 16 + 4 * j + 2] * inv, acc[c * 16 + 4 * j + 3] * inv);
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ void put_e4m3(const CUtensorMap* map, uint32_t to, int lane,
+                                         const float (&acc)[CW], float inv, int x, int y, int N) {
+  staging_begin(lane);
+#pragma unroll
+  for (int c = 0; c < CW / 16; ++c) {
+    const uint4 p = pack16_e4m3(acc, c, inv);
+    stage16(staged_piece(to, lane, 0, c), p.x, p.y, p.z, p.w);
+  }
+  staging_end(map, to, lane, 1, 128, x, y, N);
+}
+// n a multiple of 16
+__device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&acc)[CW], float inv,
+                                           int n) {
   uint8_t* dst = static_cast<uint8_t*>(out) + at;
 #pragma unroll
   for (int c = 0; c < CW / 16; ++c) {
     if (c * 16 >= n) break;
-    uint32_t p[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      p[j] = pack_e4m3x4(acc[c * 16 + 4 * j] * inv, acc[c * 16 + 4 * j + 1] * inv,
-                         acc[c * 16 + 4 * j + 2] * inv, acc[c * 16 + 4 * j + 3] * inv);
-    *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+    *reinterpret_cast<uint4*>(dst + c * 16) = pack16_e4m3(acc, c, inv);
   }
-  *scale = block_scale(m);
 }
 
 template <int BN, int OUT, bool PAIR>
 __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     fp8_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
-                       const __grid_constant__ CUtensorMap tmB, const Args a) {
+                       const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmO, const Args a) {
   using C = Cfg<BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+  uint8_t* staging = smem + C::RING_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::EPI_WARPS * STAGED);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = smem_u32(bars + C::STAGES);
   const uint32_t tfull0 = smem_u32(bars + 2 * C::STAGES);
-  const uint32_t tempty0 = smem_u32(bars + 2 * C::STAGES + C::BUFS);
-  const uint32_t drain = smem_u32(bars + 2 * C::STAGES + 2 * C::BUFS);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * C::BUFS + 1);
+  const uint32_t tempty0 = smem_u32(bars + 2 * C::STAGES + BUFS);
+  const uint32_t drain = smem_u32(bars + 2 * C::STAGES + 2 * BUFS);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * BUFS + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  float* scales = reinterpret_cast<float*>(smem + RING_BYTES + 256);  // [2 BUFS][BN / 128][128 rows]
+  float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [2 BUFS][BN / 128][128 rows]
   int* scratch = reinterpret_cast<int*>(scales + SCALE_FLOATS);
   int* tp = scratch + 40;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -218,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int b = 0; b < C::BUFS; ++b) {
+    for (int b = 0; b < BUFS; ++b) {
       mbar_init(tfull0 + 8 * b, 2);  // the products and their scales
       mbar_init(tempty0 + 8 * b, (PAIR ? 2 : 1) * C::EPI_WARPS);
     }
@@ -227,6 +327,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -256,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
   // epilogue's sums (136 + 2 * 184 = 3 * 168: the scale warp's loads in flight)
   if (warp < 4) {
     if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_par = 0;
@@ -265,29 +366,30 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         const Tile t = decode_tile(L, tp, a, C::TBM);
         const int brow = t.g * a.N + t.nt * BN + rank * C::B_ROWS;
         const int arow = static_cast<int>(t.row0) + rank * BM;
-        const int boxes = a_boxes(t.valid - rank * BM);
+        const int boxes = a_boxes<C::A_BOX>(t.valid - rank * BM);
         // a pair's copies all complete on the barrier of rank 0
         const uint32_t tx = static_cast<uint32_t>(
-            (PAIR ? a_boxes(t.valid) + a_boxes(t.valid - BM) : boxes) * A_BOX * BK + BN * BK);
+            (PAIR ? a_boxes<C::A_BOX>(t.valid) + a_boxes<C::A_BOX>(t.valid - BM) : boxes) * C::A_BOX * BK +
+            BN * BK);
         for (int kb = 0; kb < a.kblocks; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, s_abort)) {
             aborted = true;
             break;
           }
           const uint32_t st = smem_u32(ring + stage * C::STAGE_BYTES);
-          if constexpr (PAIR) {
-            const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);
+          const uint32_t fb = PAIR ? mapa_shared(full0 + 8 * stage, 0) : full0 + 8 * stage;
+          if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
-            tma_load_2d_pair(st + A_BYTES, &tmB, fb, kb * BK, brow);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d_pair(st + i * A_BOX * BK, &tmA, fb, kb * BK, arow + i * A_BOX);
-          } else {
-            const uint32_t fb = full0 + 8 * stage;
-            mbar_arrive_expect_tx(fb, tx);
-            tma_load_2d(st + A_BYTES, &tmB, fb, kb * BK, brow);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(st + i * A_BOX * BK, &tmA, fb, kb * BK, arow + i * A_BOX);
+            if constexpr (PAIR) {
+              tma_load_2d_pair(st + A_BYTES, &tmB, fb, kb * BK, brow);
+              if (boxes > 0) tma_load_2d_pair(st, &tmA, fb, kb * BK, arow);
+            } else {
+              tma_load_2d(st + A_BYTES, &tmB, fb, kb * BK, brow);
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d(st + i * C::A_BOX * BK, &tmA, fb, kb * BK, arow + i * C::A_BOX);
+            }
           }
+          __syncwarp();
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           if (++stage == C::STAGES) {
@@ -297,9 +399,9 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         }
       }
       if (aborted) {
-        set_error(a.err, kErrTimeout);
+        if (lane == 0) set_error(a.err, kErrTimeout);
         *s_abort = 1;
-        // let every copy this thread started land before the CTA releases its smem (a pair's
+        // let every copy this warp started land before the CTA releases its smem (a pair's
         // second CTA cannot watch rank 0's barrier: it waits out a fixed drain time)
         if (rank == 0) {
           for (int s = 0; s < C::STAGES; ++s)
@@ -314,23 +416,25 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       // ------------------------------------------------------------ MMA issuer
       // This one thread's instructions bound the kernel before they were cut to the bone (760
       // clocks a block, of which the tensor cores need 512): the loop runs over all blocks of
-      // all of the CTA's tiles, one turn of the ring at a time, so that every stage, accumulator
-      // and its parity is a constant.
+      // all of the CTA's tiles, one turn of the ring at a time, so that stages and accumulators
+      // are constants.
       constexpr uint32_t idesc = idesc_f32acc(C::TBM, BN, kFmtE4M3);
       const int64_t blocks = first < tiles ? static_cast<int64_t>((tiles - first + step - 1) / step) * a.kblocks : 0;
       const uint64_t desc0 = sdesc_k128(smem_u32(ring));
       uint32_t phase = 0;
       bool aborted = false;
-      for (int64_t i = 0; i < blocks && !aborted; i += C::STAGES) {
-        const int left = static_cast<int>(min(blocks - i, static_cast<int64_t>(C::STAGES)));
+      for (int64_t i = 0; i < blocks && !aborted; i += C::TURN) {
+        const int left = static_cast<int>(min(blocks - i, static_cast<int64_t>(C::TURN)));
 #pragma unroll
-        for (int st = 0; st < C::STAGES; ++st) {
+        for (int j = 0; j < C::TURN; ++j) {
           constexpr int kA = A_BYTES >> 4;
-          const int buf = st % C::BUFS;
-          const uint32_t turn = st / C::BUFS % 2;  // an odd number of turns: the parity alternates
-          if (st >= left) break;
-          if (!mbar_wait(full0 + 8 * st, phase, s_abort) ||
-              !mbar_wait(tempty0 + 8 * buf, (turn ^ (C::STAGES / C::BUFS % 2 ? phase : 0)) ^ 1, s_abort)) {
+          const int st = j % C::STAGES, buf = j % BUFS;
+          // parities: a stage or accumulator used an odd number of times a turn alternates
+          const uint32_t st_par = (j / C::STAGES % 2) ^ (C::TURN / C::STAGES % 2 ? phase : 0);
+          const uint32_t buf_par = (j / BUFS % 2) ^ (C::TURN / BUFS % 2 ? phase : 0);
+          if (j >= left) break;
+          if (!mbar_wait(full0 + 8 * st, st_par, s_abort) ||
+              !mbar_wait(tempty0 + 8 * buf, buf_par ^ 1, s_abort)) {
             aborted = true;
             break;
           }
@@ -359,7 +463,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         phase ^= 1;
       }
       if (aborted) {
-        set_error(a.err, kErrTimeout);
+        if (lane == 0) set_error(a.err, kErrTimeout);
         *s_abort = 1;
         // wait for the MMAs already issued before TMEM is freed
         if (elect_one()) {
@@ -420,8 +524,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
               for (int j = 0; j < 4; ++j) to[h * CW + 32 * j] = v.a[i][j] * v.b[i][h];
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull0 + 8 * buf);
-            if (++slot == 2 * C::BUFS) slot = 0;
-            if (++buf == C::BUFS) {
+            if (++slot == 2 * BUFS) slot = 0;
+            if (++buf == BUFS) {
               buf = 0;
               buf_phase ^= 1;
             }
@@ -442,6 +546,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + cg * CW;
     const float* my_scale = scales + cg * CW + r;
     const uint32_t free0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
+    const uint32_t to = smem_u32(staging) + (warp - 4) * STAGED;
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool aborted = false;
@@ -481,8 +586,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         } else {
           mbar_arrive_relaxed_if<PAIR>(free_bar, lane == 0);
         }
-        if (++slot == 2 * C::BUFS) slot = 0;
-        if (++buf == C::BUFS) {
+        if (++slot == 2 * BUFS) slot = 0;
+        if (++buf == BUFS) {
           buf = 0;
           buf_phase ^= 1;
         }
@@ -493,21 +598,26 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         break;
       }
       const int col = t.nt * BN + cg * CW;
-      if (row_ok && col < a.N) {
-        const int n = min(CW, a.N - col);
-        const int64_t row = t.row0 + rank * BM + r, at = row * a.N + col;
-        if (OUT == kFp8OutBf16) {
-          store_bf16(a.out, at, acc, n, a.vec32);
-        } else if (OUT == kFp8OutF32) {
-          store_f32(a.out, at, acc, n, a.vec32);
-        } else {
-          float* sc = a.out_scale + static_cast<int64_t>(col / kScaleBlock) * a.rows + row;
-          if (a.act == 2) store_e4m3<2>(a.out, at, sc, acc, n);
-          else if (a.act == 1) store_e4m3<1>(a.out, at, sc, acc, n);
-          else store_e4m3<0>(a.out, at, sc, acc, n);
-        }
+      if (!warp_ok || col >= a.N) continue;
+      const int n = min(CW, a.N - col);
+      const int row0 = static_cast<int>(t.row0) + rank * BM + quarter * 32;  // the warp's first
+      const int64_t row = row0 + lane, at = row * a.N + col;
+      const bool whole = valid >= quarter * 32 + 32;
+      if (OUT == kFp8OutE4m3) {
+        const float m = a.act == 2 ? activate<2>(acc, n) : activate<1>(acc, n);
+        const float inv = kE4m3Max / m;
+        if (row_ok) a.out_scale[static_cast<int64_t>(col / kScaleBlock) * a.rows + row] = block_scale(m);
+        if (whole) put_e4m3(&tmO, to, lane, acc, inv, col, row0, a.N);
+        else if (row_ok) store_e4m3(a.out, at, acc, inv, n);
+      } else if (OUT == kFp8OutBf16) {
+        if (whole) put_bf16(&tmO, to, lane, acc, col, row0, a.N);
+        else if (row_ok) store_bf16(a.out, at, acc, n, a.vec32);
+      } else {
+        if (whole) put_f32(&tmO, to, lane, acc, col, row0, a.N);
+        else if (row_ok) store_f32(a.out, at, acc, n, a.vec32);
       }
     }
+    if (lane == 0) bulk_store_wait();
   }
 
   __syncwarp();
@@ -532,25 +642,27 @@ template <int BN, int OUT, bool PAIR>
 static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const LaunchCtx& c) {
   using C = f8::Cfg<BN, PAIR>;
   const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, PAIR>;
-  CUtensorMap tmA, tmB;
-  if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, f8::A_BOX) ||
-      !make_tmap_1b(&tmB, p.b, static_cast<uint64_t>(p.groups) * p.N, p.K, C::B_ROWS))
+  constexpr int esize = OUT == kFp8OutF32 ? 4 : OUT == kFp8OutBf16 ? 2 : 1;
+  CUtensorMap tmA, tmB, tmO;
+  if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, C::A_BOX) ||
+      !make_tmap_1b(&tmB, p.b, static_cast<uint64_t>(p.groups) * p.N, p.K, C::B_ROWS) ||
+      !make_tmap_out(&tmO, p.out, static_cast<uint64_t>(p.rows), p.N, 32, esize))
     return cudaErrorInvalidValue;
   a.n_tiles = (p.N + BN - 1) / BN;
   // upper bound of the tile count: sum over groups of ceil(rows / TBM)
   const int64_t active = p.rows < p.groups ? p.rows : p.groups;
   const int64_t tiles = (p.offsets == nullptr ? (p.rows + C::TBM - 1) / C::TBM
                                               : p.rows / C::TBM + active) * a.n_tiles;
-  cudaError_t e = ensure_smem_limit(kernel, f8::SMEM_BYTES);
+  cudaError_t e = ensure_smem_limit(kernel, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (PAIR) {
-    const int64_t cap = max_active_pairs(kernel, C::THREADS, f8::SMEM_BYTES, c);
+    const int64_t cap = max_active_pairs(kernel, C::THREADS, C::SMEM_BYTES, c);
     return launch_kernel_pairs(kernel, dim3(static_cast<unsigned>(2 * (tiles < cap ? tiles : cap))),
-                               dim3(C::THREADS), f8::SMEM_BYTES, c, tmA, tmB, a);
+                               dim3(C::THREADS), C::SMEM_BYTES, c, tmA, tmB, tmO, a);
   }
   const int64_t grid = tiles < c.num_sms ? tiles : c.num_sms;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), f8::SMEM_BYTES,
-                       c, tmA, tmB, a);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
+                       c, tmA, tmB, tmO, a);
 }
 
 template <int BN, bool PAIR>

@@ -608,6 +608,23 @@ bool make_tmap_1b(CUtensorMap* map, const void* base, uint64_t rows, uint64_t co
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_out(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                   int esize) {
+  auto encode = get_encode_fn();
+  if (encode == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * esize};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map,
+                esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static int pick_bn(int N) {
   if (N % 256 == 0) return 256;
   if (N % 128 == 0) return 128;

@@ -339,7 +339,7 @@ struct Fp8GemmProblem {
   const void* b;          // [groups, N, K] e4m3
   const float* b_scale;   // [groups][ceil(N / 128)][ceil(K / 128)]
   int out_type;           // kFp8Out*
-  int act = 0;            // kFp8OutE4m3: 0 none, 1 ReLU, 2 GELU
+  int act = 0;            // kFp8OutE4m3: 1 ReLU, 2 GELU
   void* out;              // [rows, N]
   float* out_scale = nullptr;  // kFp8OutE4m3: [ceil(N / 128)][rows]
 };
@@ -359,6 +359,10 @@ bool make_tmap_2b(CUtensorMap* map, const void* base, uint64_t rows, uint64_t co
 // The same of 1-byte elements with a box of [box_rows, 128 columns].
 bool make_tmap_1b(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                   uint32_t box_rows);
+// For stores into a row-major [rows, cols] matrix of 1-, 2- (bf16) or 4-byte (fp32) elements:
+// boxes of box_rows rows of 128 bytes, 128-byte swizzled in shared memory.
+bool make_tmap_out(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                   int esize);
 inline bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows) {
   return make_tmap_2b(map, base, rows, cols, box_rows, 0);
