@@ -235,22 +235,25 @@ __device__ __forceinline__ void store_f32(void* out, int64_t at, const float (&a
 // Activation of the row's 128 columns (zero from column n on) and the largest magnitude.
 template <int ACT>
 __device__ __forceinline__ float activate(float (&acc)[CW], int n) {
-  float m = kAmaxFloor;
+  float m[4] = {kAmaxFloor, kAmaxFloor, kAmaxFloor, kAmaxFloor};  // four chains
 #pragma unroll
-  for (int j = 0; j < CW / 2; ++j) {
-    float &lo = acc[2 * j], &hi = acc[2 * j + 1];
-    if (2 * j >= n) {
-      lo = hi = 0.0f;
-    } else if (ACT == 1) {
+  for (int c = 0; c < CW / 8; ++c) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = acc[c * 8 + j];
+    if (ACT == 1) {
       // fmaxf would turn a NaN into 0
-      lo = lo < 0.0f ? 0.0f : lo;
-      hi = hi < 0.0f ? 0.0f : hi;
-    } else if (ACT == 2) {
-      gelu2_as7126(lo, hi, lo, hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+    } else {
+      gelu8_poly(v);
     }
-    m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[c * 8 + j] = c * 8 < n ? v[j] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = amax3_nan(m[j], acc[c * 8 + 2 * j], acc[c * 8 + 2 * j + 1]);
   }
-  return m;
+  return amax3_nan(m[0], m[1], max_nan(m[2], m[3]));
 }
 
 // 16 values of the row's scale block as e4m3.  They are fp32 sums: a product with the rounded
