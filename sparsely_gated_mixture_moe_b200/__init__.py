@@ -317,20 +317,29 @@ def _kind(t: torch.Tensor, what: str) -> int:
 
 
 def _need(what: str, t, shape, dtype, device: int):
-    """The device pointer of a contiguous CUDA tensor of this shape and type on `device`."""
+    """The device pointer of a contiguous CUDA tensor of this shape and type on `device`, or
+    None for None.  The accepting path is kept short: a call of a few microseconds on the GPU
+    takes as many such checks."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % what)
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % what) from None
     if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s %s, not %s %s" % (what, dtype, list(shape), t.dtype,
                                                           list(t.shape)))
     if t.get_device() != device:
         raise ValueError("%s must be a CUDA tensor on device %d, where the call runs"
                          % (what, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
+
+
+def _raw_stream(stream, device: int) -> int:
+    """Handle of `stream`, or of the current stream of `device` (without making a Stream)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _matrix(what: str, t, ndim: int = 2):
@@ -364,7 +373,7 @@ def moe_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, y
                            _need("residual_out", residual_out, shape, t, dev),
                            _need("y", y, shape, t, dev), _need("y_q", y_q, shape, _F8, dev),
                            _need("y_scale", y_scale, (scale_blocks(d), rows), torch.float32, dev),
-                           _need("rstd", rstd, (rows,), torch.float32, dev), _stream(stream)),
+                           _need("rstd", rstd, (rows,), torch.float32, dev), _raw_stream(stream, dev)),
            "moe_rmsnorm")
 
 
@@ -392,7 +401,7 @@ def moe_rmsnorm_backward(r, weight, rstd, dy, dx, ws=None, dresidual=None, dweig
                                     _need("dx", dx, shape, f32, dev),
                                     _need("dweight", dweight, (d,), f32, dev),
                                     None if ws is None else _workspace_ptr(ws, dev, least),
-                                    _stream(stream)), "moe_rmsnorm_backward")
+                                    _raw_stream(stream, dev)), "moe_rmsnorm_backward")
 
 
 def moe_quantize_rows_fp8(x, q, scale, stream=None):
@@ -402,7 +411,7 @@ def moe_quantize_rows_fp8(x, q, scale, stream=None):
     _check(lib.moe_quantize_rows_fp8(rows, d, kind, _need("x", x, x.shape, x.dtype, dev),
                                      _need("q", q, x.shape, _F8, dev),
                                      _need("scale", scale, (scale_blocks(d), rows), torch.float32,
-                                           dev), _stream(stream)), "moe_quantize_rows_fp8")
+                                           dev), _raw_stream(stream, dev)), "moe_quantize_rows_fp8")
 
 
 def moe_quantize_weights_fp8(w, q, scale, stream=None):
@@ -417,7 +426,7 @@ def moe_quantize_weights_fp8(w, q, scale, stream=None):
     _check(lib.moe_quantize_weights_fp8(groups, N, K, kind, _need("w", w, w.shape, w.dtype, dev),
                                         _need("q", q, w.shape, _F8, dev),
                                         _need("scale", scale, sshape, torch.float32, dev),
-                                        _stream(stream)), "moe_quantize_weights_fp8")
+                                        _raw_stream(stream, dev)), "moe_quantize_weights_fp8")
 
 
 def quantize_weights(w, stream=None):
@@ -440,7 +449,7 @@ def moe_gather_rows_fp8(cfg, x_q, x_scale, perm_src, offsets, xq_perm, xs_perm, 
                                    _need("offsets", offsets, (cfg.E + 1,), i32, dev),
                                    _need("xq_perm", xq_perm, (n, d), _F8, dev),
                                    _need("xs_perm", xs_perm, (b, n), f32, dev),
-                                   _workspace_ptr(ws, dev), _stream(stream)),
+                                   _workspace_ptr(ws, dev), _raw_stream(stream, dev)),
            "moe_gather_rows_fp8")
 
 
@@ -455,7 +464,7 @@ def moe_matmul_fp8(a_q, a_scale, b_q, b_scale, out, ws, stream=None):
                               _need("b_q", b_q, (N, K), _F8, dev),
                               _need("b_scale", b_scale, (scale_blocks(N), kb), f32, dev),
                               _need("out", out, (M, N), out.dtype, dev), kind,
-                              _workspace_ptr(ws, dev), _stream(stream)), "moe_matmul_fp8")
+                              _workspace_ptr(ws, dev), _raw_stream(stream, dev)), "moe_matmul_fp8")
 
 
 def moe_grouped_matmul_fp8(a_q, a_scale, offsets, b_q, b_scale, out, ws, stream=None):
@@ -470,7 +479,7 @@ def moe_grouped_matmul_fp8(a_q, a_scale, offsets, b_q, b_scale, out, ws, stream=
                                       _need("b_scale", b_scale, (groups, scale_blocks(N), kb), f32,
                                             dev),
                                       _need("out", out, (rows, N), out.dtype, dev), kind,
-                                      _workspace_ptr(ws, dev), _stream(stream)),
+                                      _workspace_ptr(ws, dev), _raw_stream(stream, dev)),
            "moe_grouped_matmul_fp8")
 
 
@@ -489,7 +498,7 @@ def moe_expert_ffn_fp8(cfg, x_q, x_scale, offsets, w1_q, w1_scale, w2_q, w2_scal
                                   _need("h_q", h_q, (n, f), _F8, dev),
                                   _need("h_scale", h_scale, (fb, n), f32, dev),
                                   _need("y_perm", y_perm, (n, d), f32, dev),
-                                  _workspace_ptr(ws, dev), _stream(stream)), "moe_expert_ffn_fp8")
+                                  _workspace_ptr(ws, dev), _raw_stream(stream, dev)), "moe_expert_ffn_fp8")
 
 
 def last_launch_count() -> int:

@@ -47,9 +47,15 @@ constexpr int SCALE_FLOATS = 1024;  // slots of 2 BUFS blocks
 constexpr int BUFS = 2;             // accumulators
 constexpr int STAGED = 32 * 256;    // bytes of output a warp stages: 32 rows of 256
 
-// BN columns a tile; PAIR: two CTAs share a tile of 256 rows.
-template <int BN, bool PAIR>
+// How the CTAs of a cluster share the work: none, two of them share a tile of 256 rows, or up to
+// eight share the contraction of a tile.
+enum { kSingle = 0, kPair = 1, kSplit = 2 };
+constexpr int kMaxSplits = 8;
+
+// BN columns a tile.
+template <int BN, int MODE>
 struct Cfg {
+  static constexpr bool PAIR = MODE == kPair;
   static constexpr int TBM = PAIR ? 2 * BM : BM;           // rows of a tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
@@ -63,6 +69,7 @@ struct Cfg {
   static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + EPI_WARPS * STAGED +
                                     256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
                                     4 * (MAX_GROUPS + 1 + 40);
+  static_assert(MODE != kSplit || EPI_WARPS * 32 * CW * 4 <= RING_BYTES, "partial sums fit the ring");
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
   static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS, "scales and accumulators fit");
 };
@@ -77,6 +84,7 @@ struct Args {
   float* out_scale;
   int act;    // kFp8OutE4m3: 1 ReLU, 2 GELU
   int vec32;  // output rows start on 32-byte boundaries
+  int splits;  // kSplit: CTAs that share a tile's contraction
   int* err;
 };
 
@@ -288,12 +296,13 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&
   }
 }
 
-template <int BN, int OUT, bool PAIR>
-__global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
+template <int BN, int OUT, int MODE>
+__global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
     fp8_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmO, const Args a) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, MODE>;
+  constexpr bool PAIR = C::PAIR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -313,8 +322,12 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int first = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
-  const int step = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
+  const int share = PAIR ? 2 : MODE == kSplit ? a.splits : 1;  // CTAs of a tile
+  const int first = static_cast<int>(blockIdx.x) / share, step = static_cast<int>(gridDim.x) / share;
+  // this CTA's blocks of the contraction
+  const int part = MODE == kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int kb_lo = MODE == kSplit ? a.kblocks * part / share : 0;
+  const int kb_hi = MODE == kSplit ? a.kblocks * (part + 1) / share : a.kblocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         const uint32_t tx = static_cast<uint32_t>(
             (PAIR ? a_boxes<C::A_BOX>(t.valid) + a_boxes<C::A_BOX>(t.valid - BM) : boxes) * C::A_BOX * BK +
             BN * BK);
-        for (int kb = 0; kb < a.kblocks; ++kb) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, s_abort)) {
             aborted = true;
             break;
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       // all of the CTA's tiles, one turn of the ring at a time, so that stages and accumulators
       // are constants.
       constexpr uint32_t idesc = idesc_f32acc(C::TBM, BN, kFmtE4M3);
-      const int64_t blocks = first < tiles ? static_cast<int64_t>((tiles - first + step - 1) / step) * a.kblocks : 0;
+      const int64_t blocks = first < tiles ? static_cast<int64_t>((tiles - first + step - 1) / step) * (kb_hi - kb_lo) : 0;
       const uint64_t desc0 = sdesc_k128(smem_u32(ring));
       uint32_t phase = 0;
       bool aborted = false;
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       auto load = [&](Ahead& v, const Tile& t, int kb0) {
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
-          const int kb = min(kb0 + i, a.kblocks - 1);
+          const int kb = min(kb0 + i, kb_hi - 1);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             v.a[i][j] = __ldg(a.a_scale + static_cast<int64_t>(kb) * a.rows + t.row0 +
@@ -506,16 +519,16 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       uint32_t buf_phase = 1;  // a barrier's first turn: nothing to wait for
       bool aborted = false;
       Ahead next;
-      if (first < tiles) load(next, decode_tile(first, tp, a, C::TBM), 0);
+      if (first < tiles) load(next, decode_tile(first, tp, a, C::TBM), kb_lo);
       for (int L = first; L < tiles && !aborted; L += step) {
         const Tile t = decode_tile(L, tp, a, C::TBM);
-        for (int kb0 = 0; kb0 < a.kblocks && !aborted; kb0 += GROUP) {
+        for (int kb0 = kb_lo; kb0 < kb_hi && !aborted; kb0 += GROUP) {
           const Ahead v = next;
-          if (kb0 + GROUP < a.kblocks) load(next, t, kb0 + GROUP);
-          else if (L + step < tiles) load(next, decode_tile(L + step, tp, a, C::TBM), 0);
+          if (kb0 + GROUP < kb_hi) load(next, t, kb0 + GROUP);
+          else if (L + step < tiles) load(next, decode_tile(L + step, tp, a, C::TBM), kb_lo);
 #pragma unroll
           for (int i = 0; i < GROUP; ++i) {
-            if (kb0 + i >= a.kblocks) break;
+            if (kb0 + i >= kb_hi) break;
             if (!mbar_wait(tfull0 + 8 * buf, buf_phase, s_abort)) {
               aborted = true;
               break;
@@ -560,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       float acc[CW];
 #pragma unroll
       for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
-      for (int kb = 0; kb < a.kblocks; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
         if (!mbar_wait(tfull0 + 8 * buf, buf_phase, s_abort)) {
           aborted = true;
           break;
@@ -602,6 +615,16 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       }
       const int col = t.nt * BN + cg * CW;
       if (!warp_ok || col >= a.N) continue;
+      if (MODE == kSplit) {
+        // partial sums into the ring, whose blocks are all used: piece j of thread i at 16-byte
+        // place j * threads + i
+#pragma unroll
+        for (int j = 0; j < CW / 4; ++j)
+          stage16(smem_u32(ring) + (j * C::EPI_WARPS * 32 + threadIdx.x - 128) * 16, __float_as_uint(acc[4 * j]),
+                  __float_as_uint(acc[4 * j + 1]), __float_as_uint(acc[4 * j + 2]),
+                  __float_as_uint(acc[4 * j + 3]));
+        continue;
+      }
       const int n = min(CW, a.N - col);
       const int row0 = static_cast<int>(t.row0) + rank * BM + quarter * 32;  // the warp's first
       const int64_t row = row0 + lane, at = row * a.N + col;
@@ -623,6 +646,43 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     if (lane == 0) bulk_store_wait();
   }
 
+  if constexpr (MODE == kSplit) {
+    // Each of the cluster's CTAs adds up its share of the columns over all of them, in their
+    // order.  One tile a cluster, the same for all its CTAs.
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 4 && first < tiles) {
+      const Tile t = decode_tile(first, tp, a, C::TBM);
+      const int i = threadIdx.x - 128, r = i & 127;
+      const int64_t at = (t.row0 + r) * a.N;
+      const int c0 = t.nt * BN + (i >> 7) * CW;
+      if (r < t.valid) {
+        for (int j = CW / 4 * part / share; j < CW / 4 * (part + 1) / share; ++j) {
+          if (c0 + 4 * j >= a.N) break;
+          const uint32_t from = smem_u32(ring) + (j * C::EPI_WARPS * 32 + i) * 16;
+          float4 v[kMaxSplits];
+#pragma unroll
+          for (int p = 0; p < kMaxSplits; ++p)
+            if (p < share) v[p] = ld_shared_cluster4(mapa_shared(from, p));
+          float4 sum = v[0];
+#pragma unroll
+          for (int p = 1; p < kMaxSplits; ++p)
+            if (p < share) {
+              sum.x += v[p].x;
+              sum.y += v[p].y;
+              sum.z += v[p].z;
+              sum.w += v[p].w;
+            }
+          if (OUT == kFp8OutBf16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + c0 + 4 * j) =
+                make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+          else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c0 + 4 * j) = sum;
+        }
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its sums
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -641,10 +701,17 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
 // Groups of at least this many rows on average run on CTA pairs.
 constexpr int64_t kFp8PairMinRows = 256;
 
-template <int BN, int OUT, bool PAIR>
+// Upper bound of a product's tiles of bm x bn: sum over groups of ceil(rows / bm), times n-tiles.
+static int64_t max_tiles(const Fp8GemmProblem& p, int bm, int bn) {
+  const int64_t active = p.rows < p.groups ? p.rows : p.groups;
+  const int64_t mt = p.offsets == nullptr ? (p.rows + bm - 1) / bm : p.rows / bm + active;
+  return mt * ((p.N + bn - 1) / bn);
+}
+
+template <int BN, int OUT, int MODE>
 static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const LaunchCtx& c) {
-  using C = f8::Cfg<BN, PAIR>;
-  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, PAIR>;
+  using C = f8::Cfg<BN, MODE>;
+  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, MODE>;
   constexpr int esize = OUT == kFp8OutF32 ? 4 : OUT == kFp8OutBf16 ? 2 : 1;
   CUtensorMap tmA, tmB, tmO;
   if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, C::A_BOX) ||
@@ -652,27 +719,27 @@ static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const Launc
       !make_tmap_out(&tmO, p.out, static_cast<uint64_t>(p.rows), p.N, 32, esize))
     return cudaErrorInvalidValue;
   a.n_tiles = (p.N + BN - 1) / BN;
-  // upper bound of the tile count: sum over groups of ceil(rows / TBM)
-  const int64_t active = p.rows < p.groups ? p.rows : p.groups;
-  const int64_t tiles = (p.offsets == nullptr ? (p.rows + C::TBM - 1) / C::TBM
-                                              : p.rows / C::TBM + active) * a.n_tiles;
+  const int64_t tiles = max_tiles(p, C::TBM, BN);
   cudaError_t e = ensure_smem_limit(kernel, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  if (PAIR) {
+  const dim3 block(C::THREADS);
+  if (MODE == f8::kPair) {
     const int64_t cap = max_active_pairs(kernel, C::THREADS, C::SMEM_BYTES, c);
-    return launch_kernel_pairs(kernel, dim3(static_cast<unsigned>(2 * (tiles < cap ? tiles : cap))),
-                               dim3(C::THREADS), C::SMEM_BYTES, c, tmA, tmB, tmO, a);
+    return launch_kernel_cluster(kernel, 2, dim3(static_cast<unsigned>(2 * (tiles < cap ? tiles : cap))),
+                                 block, C::SMEM_BYTES, c, tmA, tmB, tmO, a);
   }
-  const int64_t grid = tiles < c.num_sms ? tiles : c.num_sms;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
-                       c, tmA, tmB, tmO, a);
+  if (MODE == f8::kSplit)
+    return launch_kernel_cluster(kernel, a.splits, dim3(static_cast<unsigned>(tiles * a.splits)), block,
+                                 C::SMEM_BYTES, c, tmA, tmB, tmO, a);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles < c.num_sms ? tiles : c.num_sms)), block,
+                       C::SMEM_BYTES, c, tmA, tmB, tmO, a);
 }
 
-template <int BN, bool PAIR>
+template <int BN, int MODE>
 static cudaError_t launch_out(const Fp8GemmProblem& p, const f8::Args& a, const LaunchCtx& c) {
-  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, PAIR>(p, a, c);
-  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, PAIR>(p, a, c);
-  return launch_tiles<BN, kFp8OutE4m3, PAIR>(p, a, c);
+  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, MODE>(p, a, c);
+  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, MODE>(p, a, c);
+  return launch_tiles<BN, kFp8OutE4m3, MODE>(p, a, c);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
@@ -693,9 +760,21 @@ cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
   const int64_t row_bytes = static_cast<int64_t>(p.N) * (p.out_type == kFp8OutF32 ? 4 : 2);
   a.vec32 = row_bytes % 32 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
   a.err = c.err;
-  if (p.N <= 128) return launch_out<128, false>(p, a, c);
-  if (p.rows >= kFp8PairMinRows * p.groups) return launch_out<256, true>(p, a, c);
-  return launch_out<256, false>(p, a, c);
+  a.splits = 1;
+  // Pairs for groups that fill their tiles, as long as the pairs fill the device; then the
+  // widest tile that does; below that tiles of 128 columns, and clusters that split the
+  // contraction among as many CTAs as there are SMs for, two blocks each at least (an e4m3
+  // output needs all sums of a block of columns in one thread and is not split).
+  if (p.rows >= kFp8PairMinRows * p.groups && 2 * max_tiles(p, 2 * f8::BM, 256) >= c.num_sms)
+    return launch_out<256, f8::kPair>(p, a, c);
+  if (max_tiles(p, f8::BM, 256) >= c.num_sms) return launch_out<256, f8::kSingle>(p, a, c);
+  const int64_t tiles = max_tiles(p, f8::BM, 128);
+  if (p.out_type != kFp8OutE4m3)
+    while (a.splits < f8::kMaxSplits && tiles * a.splits * 2 <= c.num_sms && a.kblocks >= a.splits * 4)
+      a.splits *= 2;
+  if (a.splits == 1) return launch_out<128, f8::kSingle>(p, a, c);
+  return p.out_type == kFp8OutBf16 ? launch_tiles<128, kFp8OutBf16, f8::kSplit>(p, a, c)
+                                   : launch_tiles<128, kFp8OutF32, f8::kSplit>(p, a, c);
 }
 
 }  // namespace moe

@@ -72,11 +72,12 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   return e;
 }
 
-// As launch_kernel, for a kernel whose CTAs run in clusters of two (grid.x even): the two
-// CTAs of a cluster are co-scheduled on a pair of SMs and share a tensor-core product.
+// As launch_kernel, for a kernel whose CTAs run in clusters of `cluster` consecutive ones
+// (grid.x a multiple): the CTAs of a cluster are co-scheduled and reach each other's shared
+// memory.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                const LaunchCtx& c, Args... args) {
+cudaError_t launch_kernel_cluster(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block,
+                                  size_t smem, const LaunchCtx& c, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -86,7 +87,7 @@ cudaError_t launch_kernel_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -94,6 +95,13 @@ cudaError_t launch_kernel_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block,
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   ++*c.launches;
   return e;
+}
+
+// Clusters of two: a pair of CTAs shares a tensor-core product.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                const LaunchCtx& c, Args... args) {
+  return launch_kernel_cluster(kernel, 2, grid, block, smem, c, args...);
 }
 
 // Clusters of two CTAs of a kernel that fit on the device at once (a persistent grid larger
