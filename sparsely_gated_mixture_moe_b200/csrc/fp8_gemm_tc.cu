@@ -39,36 +39,40 @@ namespace f8 {
 
 constexpr int BM = 128;
 constexpr int BK = 128;  // bytes of a k-block's rows: one scale block of the contraction
-constexpr int A_BYTES = BM * BK;
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
-constexpr int CW = 128;    // columns of an epilogue thread: a scale block
+constexpr int CW = 128;    // most columns of an epilogue thread: a scale block
 constexpr int SCALE_FLOATS = 1024;  // slots of 2 BUFS blocks
 constexpr int BUFS = 2;             // accumulators
 constexpr int STAGED = 32 * 256;    // bytes of output a warp stages: 32 rows of 256
+// A warp with at most this many rows spreads each row's scale block over its lanes (below).
+constexpr int kFewRows = 8;
 
 // How the CTAs of a cluster share the work: none, two of them share a tile of 256 rows, or up to
 // eight share the contraction of a tile.
 enum { kSingle = 0, kPair = 1, kSplit = 2 };
 constexpr int kMaxSplits = 8;
 
-// BN columns a tile.
-template <int BN, int MODE>
+// BN columns a tile; ROWS of A a CTA holds: 128, or 32 for few rows a group, whose weights then
+// have most of the ring.  The MMA's other 96 rows are whatever follows in the stage.
+template <int BN, int MODE, int ROWS>
 struct Cfg {
   static constexpr bool PAIR = MODE == kPair;
-  static constexpr int TBM = PAIR ? 2 * BM : BM;           // rows of a tile
+  static constexpr int TBM = PAIR ? 2 * ROWS : ROWS;       // rows of a tile
+  static constexpr int A_BYTES = ROWS * BK;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
-  static constexpr int STAGES = !PAIR && BN == 256 ? 3 : 4;
+  static constexpr int STAGES = ROWS == 32 ? (BN == 256 ? 5 : 8) : !PAIR && BN == 256 ? 3 : 4;
   static constexpr int TURN = STAGES % BUFS == 0 ? STAGES : STAGES * BUFS;  // of stages and accumulators
-  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 KB, or 144 (single, BN = 256)
-  // rows of A in one copy: a small group's tile needs few
-  static constexpr int A_BOX = PAIR ? BM : 32;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 to 180 KB
+  static constexpr int A_BOX = PAIR ? ROWS : 32;           // rows of A in one copy: ragged tiles need few
   static constexpr int EPI_WARPS = BN / CW * 4;            // 8 or 4
+  static constexpr int STAGING = BN / CW * (ROWS == 32 ? kFewRows * CW * 4 : 4 * STAGED);
   static constexpr int THREADS = 128 + EPI_WARPS * 32;
-  static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + EPI_WARPS * STAGED +
+  static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + STAGING +
                                     256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
                                     4 * (MAX_GROUPS + 1 + 40);
+  static_assert(STAGE_BYTES >= BM * BK, "the MMA's 128 rows stay in the stage");
   static_assert(MODE != kSplit || EPI_WARPS * 32 * CW * 4 <= RING_BYTES, "partial sums fit the ring");
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
   static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS, "scales and accumulators fit");
@@ -254,7 +258,7 @@ __device__ __forceinline__ float activate(float (&acc)[CW], int n) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
     } else {
-      gelu8_poly(v);
+      gelu_poly<4>(v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[c * 8 + j] = c * 8 < n ? v[j] : 0.0f;
@@ -296,19 +300,59 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&
   }
 }
 
-template <int BN, int OUT, int MODE>
-__global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
+// The e4m3 output of a warp with at most kFewRows rows, each row's scale block spread over the
+// lanes: with a thread a row most lanes had nothing to do, and one row cost the 5,000 clocks of
+// 32.
+__device__ __forceinline__ void put_few_e4m3(const Args& a, uint8_t* to, int lane,
+                                             const float (&acc)[CW], int rows, int n, int row0,
+                                             int col) {
+  if (lane == 0) bulk_store_wait_read();  // an earlier tile's rows may be on their way from here
+  __syncwarp();
+  float* stage = reinterpret_cast<float*>(to);
+  if (lane < rows) {
+#pragma unroll
+    for (int j = 0; j < CW / 4; ++j)
+      *reinterpret_cast<float4*>(stage + lane * CW + 4 * (j ^ lane)) =
+          make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+  }
+  __syncwarp();
+  for (int r = 0; r < rows; ++r) {
+    const float4 z = *reinterpret_cast<const float4*>(stage + r * CW + 4 * (lane ^ r));
+    float v[4] = {z.x, z.y, z.z, z.w};
+    if (a.act == 2) {
+      gelu_poly<2>(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+    }
+    const bool in = lane * 4 < n;
+    float m = in ? amax3_nan(v[0], v[1], amax3_nan(v[2], v[3], kAmaxFloor)) : kAmaxFloor;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float inv = kE4m3Max / m;
+    const int64_t row = row0 + r;
+    if (in)
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + row * a.N + col + lane * 4) =
+          pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    if (lane == 0) a.out_scale[static_cast<int64_t>(col / kScaleBlock) * a.rows + row] = block_scale(m);
+  }
+  __syncwarp();  // read before the next tile's rows are written
+}
+
+template <int BN, int OUT, int MODE, int ROWS>
+__global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     fp8_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmO, const Args a) {
-  using C = Cfg<BN, MODE>;
+  using C = Cfg<BN, MODE, ROWS>;
   constexpr bool PAIR = C::PAIR;
+  constexpr int A_BYTES = C::A_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;
   uint8_t* staging = smem + C::RING_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::EPI_WARPS * STAGED);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STAGING);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = smem_u32(bars + C::STAGES);
   const uint32_t tfull0 = smem_u32(bars + 2 * C::STAGES);
@@ -381,8 +425,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
       for (int L = first; L < tiles && !aborted; L += step) {
         const Tile t = decode_tile(L, tp, a, C::TBM);
         const int brow = t.g * a.N + t.nt * BN + rank * C::B_ROWS;
-        const int arow = static_cast<int>(t.row0) + rank * BM;
-        const int boxes = a_boxes<C::A_BOX>(t.valid - rank * BM);
+        const int arow = static_cast<int>(t.row0) + rank * ROWS;
+        const int boxes = a_boxes<C::A_BOX>(t.valid - rank * ROWS);
         // a pair's copies all complete on the barrier of rank 0
         const uint32_t tx = static_cast<uint32_t>(
             (PAIR ? a_boxes<C::A_BOX>(t.valid) + a_boxes<C::A_BOX>(t.valid - BM) : boxes) * C::A_BOX * BK +
@@ -434,7 +478,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
       // clocks a block, of which the tensor cores need 512): the loop runs over all blocks of
       // all of the CTA's tiles, one turn of the ring at a time, so that stages and accumulators
       // are constants.
-      constexpr uint32_t idesc = idesc_f32acc(C::TBM, BN, kFmtE4M3);
+      constexpr uint32_t idesc = idesc_f32acc(PAIR ? 2 * BM : BM, BN, kFmtE4M3);
       const int64_t blocks = first < tiles ? static_cast<int64_t>((tiles - first + step - 1) / step) * (kb_hi - kb_lo) : 0;
       const uint64_t desc0 = sdesc_k128(smem_u32(ring));
       uint32_t phase = 0;
@@ -493,18 +537,18 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
       // ------------------------------------------------------------ scales
       // GROUP blocks at a time: the next group's loads are in flight while this one's wait
       // for their accumulators.
-      constexpr int GROUP = 4, HALVES = BN / CW;
+      constexpr int GROUP = 4, HALVES = BN / CW, ROW4 = ROWS / 32;
       struct Ahead {
-        float a[GROUP][4], b[GROUP][HALVES];
+        float a[GROUP][ROW4], b[GROUP][HALVES];
       };
       auto load = [&](Ahead& v, const Tile& t, int kb0) {
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
           const int kb = min(kb0 + i, kb_hi - 1);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < ROW4; ++j)
             v.a[i][j] = __ldg(a.a_scale + static_cast<int64_t>(kb) * a.rows + t.row0 +
-                              min(rank * BM + lane + 32 * j, t.valid - 1));
+                              min(rank * ROWS + lane + 32 * j, t.valid - 1));
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
             const int nb = min(t.nt * HALVES + h, a.nblocks - 1);
@@ -533,11 +577,11 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
               aborted = true;
               break;
             }
-            float* to = scales + slot * BN + lane;
+            float* to = scales + slot * (HALVES * BM) + lane;
 #pragma unroll
             for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) to[h * CW + 32 * j] = v.a[i][j] * v.b[i][h];
+              for (int j = 0; j < ROW4; ++j) to[h * BM + 32 * j] = v.a[i][j] * v.b[i][h];
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull0 + 8 * buf);
             if (++slot == 2 * BUFS) slot = 0;
@@ -557,18 +601,19 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
     if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;       // TMEM lane quarter this warp may read
-    const int cg = (warp - 4) >> 2;     // which 128 columns of the tile
+    const int cg = (warp - 4) >> 2;     // which columns of the tile
     const int r = quarter * 32 + lane;
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + cg * CW;
-    const float* my_scale = scales + cg * CW + r;
+    const float* my_scale = scales + cg * BM + r;
     const uint32_t free0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
     const uint32_t to = smem_u32(staging) + (warp - 4) * STAGED;
+    uint8_t* few_at = staging + (ROWS == 32 ? cg * kFewRows * CW * 4 : (warp - 4) * STAGED);
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool aborted = false;
     for (int L = first; L < tiles && !aborted; L += step) {
       const Tile t = decode_tile(L, tp, a, C::TBM);
-      const int valid = t.valid - rank * BM;
+      const int valid = t.valid - rank * ROWS;
       const bool row_ok = r < valid, warp_ok = quarter * 32 < valid;
       float acc[CW];
 #pragma unroll
@@ -626,16 +671,21 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
         continue;
       }
       const int n = min(CW, a.N - col);
-      const int row0 = static_cast<int>(t.row0) + rank * BM + quarter * 32;  // the warp's first
+      const int row0 = static_cast<int>(t.row0) + rank * ROWS + quarter * 32;  // the warp's first
       const int64_t row = row0 + lane, at = row * a.N + col;
-      const bool whole = valid >= quarter * 32 + 32;
-      if (OUT == kFp8OutE4m3) {
+      const bool whole = ROWS == BM && valid >= quarter * 32 + 32;  // else there is no room to stage
+      if constexpr (OUT == kFp8OutE4m3) {
+        const int few = min(32, valid - quarter * 32);
+        if (few <= kFewRows) {
+          put_few_e4m3(a, few_at, lane, acc, few, n, row0, col);
+          continue;
+        }
         const float m = a.act == 2 ? activate<2>(acc, n) : activate<1>(acc, n);
         const float inv = kE4m3Max / m;
         if (row_ok) a.out_scale[static_cast<int64_t>(col / kScaleBlock) * a.rows + row] = block_scale(m);
         if (whole) put_e4m3(&tmO, to, lane, acc, inv, col, row0, a.N);
         else if (row_ok) store_e4m3(a.out, at, acc, inv, n);
-      } else if (OUT == kFp8OutBf16) {
+      } else if constexpr (OUT == kFp8OutBf16) {
         if (whole) put_bf16(&tmO, to, lane, acc, col, row0, a.N);
         else if (row_ok) store_bf16(a.out, at, acc, n, a.vec32);
       } else {
@@ -700,6 +750,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
 
 // Groups of at least this many rows on average run on CTA pairs.
 constexpr int64_t kFp8PairMinRows = 256;
+// Groups of at most this many on average have tiles of 32 rows.
+constexpr int64_t kFp8FewRows = 16;
 
 // Upper bound of a product's tiles of bm x bn: sum over groups of ceil(rows / bm), times n-tiles.
 static int64_t max_tiles(const Fp8GemmProblem& p, int bm, int bn) {
@@ -708,10 +760,10 @@ static int64_t max_tiles(const Fp8GemmProblem& p, int bm, int bn) {
   return mt * ((p.N + bn - 1) / bn);
 }
 
-template <int BN, int OUT, int MODE>
+template <int BN, int OUT, int MODE, int ROWS>
 static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const LaunchCtx& c) {
-  using C = f8::Cfg<BN, MODE>;
-  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, MODE>;
+  using C = f8::Cfg<BN, MODE, ROWS>;
+  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, MODE, ROWS>;
   constexpr int esize = OUT == kFp8OutF32 ? 4 : OUT == kFp8OutBf16 ? 2 : 1;
   CUtensorMap tmA, tmB, tmO;
   if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, C::A_BOX) ||
@@ -735,11 +787,11 @@ static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const Launc
                        C::SMEM_BYTES, c, tmA, tmB, tmO, a);
 }
 
-template <int BN, int MODE>
+template <int BN, int MODE, int ROWS>
 static cudaError_t launch_out(const Fp8GemmProblem& p, const f8::Args& a, const LaunchCtx& c) {
-  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, MODE>(p, a, c);
-  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, MODE>(p, a, c);
-  return launch_tiles<BN, kFp8OutE4m3, MODE>(p, a, c);
+  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, MODE, ROWS>(p, a, c);
+  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, MODE, ROWS>(p, a, c);
+  return launch_tiles<BN, kFp8OutE4m3, MODE, ROWS>(p, a, c);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
@@ -766,15 +818,24 @@ cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
   // contraction among as many CTAs as there are SMs for, two blocks each at least (an e4m3
   // output needs all sums of a block of columns in one thread and is not split).
   if (p.rows >= kFp8PairMinRows * p.groups && 2 * max_tiles(p, 2 * f8::BM, 256) >= c.num_sms)
-    return launch_out<256, f8::kPair>(p, a, c);
-  if (max_tiles(p, f8::BM, 256) >= c.num_sms) return launch_out<256, f8::kSingle>(p, a, c);
-  const int64_t tiles = max_tiles(p, f8::BM, 128);
+    return launch_out<256, f8::kPair, f8::BM>(p, a, c);
+  // Tiles of 32 rows, whose weights have 144 to 160 KB of shared memory on their way instead of
+  // 64 to 96, for groups that mostly fit in one.
+  const bool few = p.offsets == nullptr ? p.rows <= 32 : p.rows <= kFp8FewRows * p.groups;
+  const int bm = few ? 32 : f8::BM;
+  if (max_tiles(p, bm, 256) >= (few ? c.num_sms / 2 : c.num_sms))
+    return few ? launch_out<256, f8::kSingle, 32>(p, a, c) : launch_out<256, f8::kSingle, f8::BM>(p, a, c);
+  const int64_t tiles = max_tiles(p, bm, 128);
   if (p.out_type != kFp8OutE4m3)
     while (a.splits < f8::kMaxSplits && tiles * a.splits * 2 <= c.num_sms && a.kblocks >= a.splits * 4)
       a.splits *= 2;
-  if (a.splits == 1) return launch_out<128, f8::kSingle>(p, a, c);
-  return p.out_type == kFp8OutBf16 ? launch_tiles<128, kFp8OutBf16, f8::kSplit>(p, a, c)
-                                   : launch_tiles<128, kFp8OutF32, f8::kSplit>(p, a, c);
+  if (a.splits == 1)
+    return few ? launch_out<128, f8::kSingle, 32>(p, a, c) : launch_out<128, f8::kSingle, f8::BM>(p, a, c);
+  if (p.out_type == kFp8OutBf16)
+    return few ? launch_tiles<128, kFp8OutBf16, f8::kSplit, 32>(p, a, c)
+               : launch_tiles<128, kFp8OutBf16, f8::kSplit, f8::BM>(p, a, c);
+  return few ? launch_tiles<128, kFp8OutF32, f8::kSplit, 32>(p, a, c)
+             : launch_tiles<128, kFp8OutF32, f8::kSplit, f8::BM>(p, a, c);
 }
 
 }  // namespace moe
