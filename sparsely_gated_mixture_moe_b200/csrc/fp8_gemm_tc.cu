@@ -43,8 +43,6 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr int CW = 128;    // most columns of an epilogue thread: a scale block
 constexpr int SCALE_FLOATS = 1024;  // slots of 2 BUFS blocks
-constexpr int BUFS = 2;             // accumulators
-constexpr int STAGED = 32 * 256;    // bytes of output a warp stages: 32 rows of 256
 // A warp with at most this many rows spreads each row's scale block over its lanes (below).
 constexpr int kFewRows = 8;
 
@@ -63,16 +61,20 @@ struct Cfg {
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
   static constexpr int STAGES = ROWS == 32 ? (BN == 256 ? 5 : 8) : !PAIR && BN == 256 ? 3 : 4;
+  static constexpr int BUFS = TMEM_COLS / BN;              // accumulators: 2 or 4
   static constexpr int TURN = STAGES % BUFS == 0 ? STAGES : STAGES * BUFS;  // of stages and accumulators
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 to 180 KB
   static constexpr int A_BOX = PAIR ? ROWS : 32;           // rows of A in one copy: ragged tiles need few
   static constexpr int EPI_WARPS = BN / CW * 4;            // 8 or 4
+  // bytes of output a warp stages: 32 rows of 512 (all columns as fp32), or of 256 at a time
+  static constexpr int STAGED = 32 * (BN == 128 ? 512 : 256);
   static constexpr int STAGING = BN / CW * (ROWS == 32 ? kFewRows * CW * 4 : 4 * STAGED);
   static constexpr int THREADS = 128 + EPI_WARPS * 32;
   static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + STAGING +
                                     256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
                                     4 * (MAX_GROUPS + 1 + 40);
   static_assert(STAGE_BYTES >= BM * BK, "the MMA's 128 rows stay in the stage");
+  static_assert(MODE != kSplit || BN == CW, "one 128-column block a tile");
   static_assert(MODE != kSplit || EPI_WARPS * 32 * CW * 4 <= RING_BYTES, "partial sums fit the ring");
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
   static_assert(2 * BUFS * BN <= SCALE_FLOATS && BUFS * BN <= TMEM_COLS, "scales and accumulators fit");
@@ -140,12 +142,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
 __device__ __forceinline__ void bulk_store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Until this thread's stores have read shared memory, or are complete.
+// Until this thread's stores have read shared memory.
 __device__ __forceinline__ void bulk_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 // Makes this thread's writes to shared memory visible to bulk copies.
 __device__ __forceinline__ void fence_async_shared() {
@@ -191,17 +190,20 @@ __device__ __forceinline__ void put_bf16(const CUtensorMap* map, uint32_t to, in
             pack_bf16x2(acc[c * 8 + 6], acc[c * 8 + 7]));
   staging_end(map, to, lane, 2, 64, x, y, N);
 }
+// ROOM: bytes of the staging place; 8 KB take the columns in two halves.
+template <int ROOM>
 __device__ __forceinline__ void put_f32(const CUtensorMap* map, uint32_t to, int lane,
                                         const float (&acc)[CW], int x, int y, int N) {
+  constexpr int COLS = ROOM / 128;  // columns at a time: 32 rows of fp32
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < CW / COLS; ++h) {
     staging_begin(lane);
 #pragma unroll
-    for (int c = 0; c < CW / 8; ++c)
-      stage16(staged_piece(to, lane, c / 8, c % 8), __float_as_uint(acc[h * 64 + c * 4]),
-              __float_as_uint(acc[h * 64 + c * 4 + 1]), __float_as_uint(acc[h * 64 + c * 4 + 2]),
-              __float_as_uint(acc[h * 64 + c * 4 + 3]));
-    staging_end(map, to, lane, 2, 32, x + h * 64, y, N);
+    for (int c = 0; c < COLS / 4; ++c)
+      stage16(staged_piece(to, lane, c / 8, c % 8), __float_as_uint(acc[h * COLS + c * 4]),
+              __float_as_uint(acc[h * COLS + c * 4 + 1]), __float_as_uint(acc[h * COLS + c * 4 + 2]),
+              __float_as_uint(acc[h * COLS + c * 4 + 3]));
+    staging_end(map, to, lane, COLS / 32, 32, x + h * COLS, y, N);
   }
 }
 
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmO, const Args a) {
   using C = Cfg<BN, MODE, ROWS>;
   constexpr bool PAIR = C::PAIR;
-  constexpr int A_BYTES = C::A_BYTES;
+  constexpr int A_BYTES = C::A_BYTES, BUFS = C::BUFS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -606,8 +608,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + cg * CW;
     const float* my_scale = scales + cg * BM + r;
     const uint32_t free0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
-    const uint32_t to = smem_u32(staging) + (warp - 4) * STAGED;
-    uint8_t* few_at = staging + (ROWS == 32 ? cg * kFewRows * CW * 4 : (warp - 4) * STAGED);
+    const uint32_t to = smem_u32(staging) + (warp - 4) * C::STAGED;
+    uint8_t* few_at = staging + (ROWS == 32 ? cg * kFewRows * CW * 4 : (warp - 4) * C::STAGED);
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool aborted = false;
@@ -689,11 +691,11 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
         if (whole) put_bf16(&tmO, to, lane, acc, col, row0, a.N);
         else if (row_ok) store_bf16(a.out, at, acc, n, a.vec32);
       } else {
-        if (whole) put_f32(&tmO, to, lane, acc, col, row0, a.N);
+        if (whole) put_f32<C::STAGED>(&tmO, to, lane, acc, col, row0, a.N);
         else if (row_ok) store_f32(a.out, at, acc, n, a.vec32);
       }
     }
-    if (lane == 0) bulk_store_wait();
+    if (lane == 0) bulk_store_wait_read();  // the CTA's shared memory is needed until then
   }
 
   if constexpr (MODE == kSplit) {
@@ -703,32 +705,31 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     cluster_sync_all();
     if (warp >= 4 && first < tiles) {
       const Tile t = decode_tile(first, tp, a, C::TBM);
-      const int i = threadIdx.x - 128, r = i & 127;
-      const int64_t at = (t.row0 + r) * a.N;
-      const int c0 = t.nt * BN + (i >> 7) * CW;
-      if (r < t.valid) {
-        for (int j = CW / 4 * part / share; j < CW / 4 * (part + 1) / share; ++j) {
-          if (c0 + 4 * j >= a.N) break;
-          const uint32_t from = smem_u32(ring) + (j * C::EPI_WARPS * 32 + i) * 16;
-          float4 v[kMaxSplits];
+      const int j0 = CW / 4 * part / share, width = CW / 4 / share;  // four columns each
+      // a thread for four columns of a row, all loads of the cluster's sums in flight at once
+      for (int i = threadIdx.x - 128; i < t.valid * width; i += C::EPI_WARPS * 32) {
+        const int r = i / width, j = j0 + i % width, col = t.nt * BN + 4 * j;
+        if (col >= a.N) continue;
+        const uint32_t from = smem_u32(ring) + (j * C::EPI_WARPS * 32 + r) * 16;
+        float4 v[kMaxSplits];
 #pragma unroll
-          for (int p = 0; p < kMaxSplits; ++p)
-            if (p < share) v[p] = ld_shared_cluster4(mapa_shared(from, p));
-          float4 sum = v[0];
+        for (int p = 0; p < kMaxSplits; ++p)
+          if (p < share) v[p] = ld_shared_cluster4(mapa_shared(from, p));
+        float4 sum = v[0];
 #pragma unroll
-          for (int p = 1; p < kMaxSplits; ++p)
-            if (p < share) {
-              sum.x += v[p].x;
-              sum.y += v[p].y;
-              sum.z += v[p].z;
-              sum.w += v[p].w;
-            }
-          if (OUT == kFp8OutBf16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + c0 + 4 * j) =
-                make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-          else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c0 + 4 * j) = sum;
-        }
+        for (int p = 1; p < kMaxSplits; ++p)
+          if (p < share) {
+            sum.x += v[p].x;
+            sum.y += v[p].y;
+            sum.z += v[p].z;
+            sum.w += v[p].w;
+          }
+        const int64_t at = (t.row0 + r) * a.N + col;
+        if (OUT == kFp8OutBf16)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+              make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = sum;
       }
     }
     cluster_sync_all();  // no CTA leaves while another reads its sums
