@@ -58,7 +58,8 @@ def quantize_weights(w):
 
 
 def rows_value(q, scale):
-    return np.asarray(q, np.float64) * np.repeat(np.asarray(scale, np.float64).T, BLOCK, 1)[:, : q.shape[1]]
+    with np.errstate(invalid="ignore"):  # 0 * inf: a block that held an infinity
+        return np.asarray(q, np.float64) * np.repeat(np.asarray(scale, np.float64).T, BLOCK, 1)[:, : q.shape[1]]
 
 
 def weights_value(q, scale):

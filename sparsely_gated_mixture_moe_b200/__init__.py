@@ -312,6 +312,8 @@ def scale_blocks(n: int) -> int:
 def _kind(t: torch.Tensor, what: str) -> int:
     try:
         return _KIND[t.dtype]
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % what) from None
     except KeyError:
         raise ValueError("%s must be bf16 or fp32, not %s" % (what, t.dtype)) from None
 
@@ -337,17 +339,33 @@ def _need(what: str, t, shape, dtype, device: int):
     raise ValueError("%s must be contiguous" % what)
 
 
+def _here(what: str, t) -> int:
+    """The current device, where t must be."""
+    try:
+        device = t.get_device()
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % what) from None
+    if device < 0:
+        raise ValueError("%s must be a CUDA tensor (libmoe has no CPU path)" % what)
+    if device != torch.cuda.current_device():
+        raise ValueError("%s is on device %d, the call runs on the current device %d"
+                         % (what, device, torch.cuda.current_device()))
+    return device
+
+
 def _raw_stream(stream, device: int) -> int:
     """Handle of `stream`, or of the current stream of `device` (without making a Stream)."""
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _matrix(what: str, t, ndim: int = 2):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % what)
-    if t.dim() != ndim:
-        raise ValueError("%s must have %d dimensions, not %d" % (what, ndim, t.dim()))
-    return t.shape
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % what) from None
+    if len(shape) != ndim:
+        raise ValueError("%s must have %d dimensions, not %d" % (what, ndim, len(shape)))
+    return shape
 
 
 def _workspace_ptr(ws, device: int, least: int = 256):
@@ -364,8 +382,9 @@ def moe_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, y
                 y_scale=None, rstd=None, stream=None):
     """r = x + residual (to residual_out), y = r / sqrt(mean(r^2) + eps) * weight into y (x's
     type) and / or (y_q, y_scale) (e4m3 with block scales); rstd [rows] for the backward."""
+    dev = _here("x", x)
     rows, d = _matrix("x", x)
-    t, dev = x.dtype, torch.cuda.current_device()
+    t = x.dtype
     kind, shape = _kind(x, "x"), x.shape
     _check(lib.moe_rmsnorm(rows, d, kind, eps, _need("x", x, shape, t, dev),
                            _need("residual", residual, shape, t, dev),
@@ -389,8 +408,9 @@ def moe_rmsnorm_backward(r, weight, rstd, dy, dx, ws=None, dresidual=None, dweig
                          stream=None):
     """Gradients of moe_rmsnorm: dx of r (so of x and of the residual), dweight of weight (then
     ws is needed).  r is the forward's residual_out, or x where there was no residual."""
+    dev = _here("r", r)
     rows, d = _matrix("r", r)
-    dev, f32, shape = torch.cuda.current_device(), torch.float32, r.shape
+    f32, shape = torch.float32, r.shape
     kind = _kind(r, "r")
     least = int(lib.moe_rmsnorm_backward_workspace_size(rows, d)) if dweight is not None else 0
     _check(lib.moe_rmsnorm_backward(rows, d, kind, _need("r", r, shape, r.dtype, dev),
@@ -406,8 +426,9 @@ def moe_rmsnorm_backward(r, weight, rstd, dy, dx, ws=None, dresidual=None, dweig
 
 def moe_quantize_rows_fp8(x, q, scale, stream=None):
     """Rows x [rows, d] (bf16 or fp32) as e4m3 q with scale [scale_blocks(d), rows]."""
+    dev = _here("x", x)
     rows, d = _matrix("x", x)
-    dev, kind = torch.cuda.current_device(), _kind(x, "x")
+    kind = _kind(x, "x")
     _check(lib.moe_quantize_rows_fp8(rows, d, kind, _need("x", x, x.shape, x.dtype, dev),
                                      _need("q", q, x.shape, _F8, dev),
                                      _need("scale", scale, (scale_blocks(d), rows), torch.float32,
@@ -417,11 +438,12 @@ def moe_quantize_rows_fp8(x, q, scale, stream=None):
 def moe_quantize_weights_fp8(w, q, scale, stream=None):
     """Weights w [N, K] or [groups, N, K] as e4m3 q (same shape) with a scale for each block
     of 128 x 128, [.., scale_blocks(N), scale_blocks(K)]."""
-    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
-        raise ValueError("w must be a tensor of two or three dimensions")
+    dev = _here("w", w)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must have two or three dimensions, not %d" % w.dim())
     N, K = w.shape[-2:]
     groups = w.shape[0] if w.dim() == 3 else 1
-    dev, kind = torch.cuda.current_device(), _kind(w, "w")
+    kind = _kind(w, "w")
     sshape = (*w.shape[:-2], scale_blocks(N), scale_blocks(K))
     _check(lib.moe_quantize_weights_fp8(groups, N, K, kind, _need("w", w, w.shape, w.dtype, dev),
                                         _need("q", q, w.shape, _F8, dev),
@@ -441,7 +463,7 @@ def quantize_weights(w, stream=None):
 
 def moe_gather_rows_fp8(cfg, x_q, x_scale, perm_src, offsets, xq_perm, xs_perm, ws, stream=None):
     """Permuted row s < offsets[E] is token row perm_src[s] // k of x_q, with its scales."""
-    T, d, n, dev = cfg.T, cfg.d_model, cfg.T * cfg.k, torch.cuda.current_device()
+    T, d, n, dev = cfg.T, cfg.d_model, cfg.T * cfg.k, _here("x_q", x_q)
     f32, i32, b = torch.float32, torch.int32, scale_blocks(d)
     _check(lib.moe_gather_rows_fp8(ctypes.byref(cfg), _need("x_q", x_q, (T, d), _F8, dev),
                                    _need("x_scale", x_scale, (b, T), f32, dev),
@@ -456,8 +478,9 @@ def moe_gather_rows_fp8(cfg, x_q, x_scale, perm_src, offsets, xq_perm, xs_perm, 
 def moe_matmul_fp8(a_q, a_scale, b_q, b_scale, out, ws, stream=None):
     """out [M, N] (fp32 or bf16) = a . b^T of e4m3 a_q [M, K] and b_q [N, K] with their block
     scales [scale_blocks(K), M] and [scale_blocks(N), scale_blocks(K)]."""
+    dev = _here("a_q", a_q)
     M, K = _matrix("a_q", a_q)
-    N, dev, f32 = _matrix("b_q", b_q)[0], torch.cuda.current_device(), torch.float32
+    N, f32 = _matrix("b_q", b_q)[0], torch.float32
     kb, kind = scale_blocks(K), _kind(out, "out")
     _check(lib.moe_matmul_fp8(M, N, K, _need("a_q", a_q, (M, K), _F8, dev),
                               _need("a_scale", a_scale, (kb, M), f32, dev),
@@ -469,9 +492,10 @@ def moe_matmul_fp8(a_q, a_scale, b_q, b_scale, out, ws, stream=None):
 
 def moe_grouped_matmul_fp8(a_q, a_scale, offsets, b_q, b_scale, out, ws, stream=None):
     """Rows [offsets[g], offsets[g+1]) of out = those of a . b[g]^T; b_q [groups, N, K]."""
+    dev = _here("a_q", a_q)
     rows, K = _matrix("a_q", a_q)
     groups, N, _ = _matrix("b_q", b_q, 3)
-    dev, f32, kb, kind = torch.cuda.current_device(), torch.float32, scale_blocks(K), _kind(out, "out")
+    f32, kb, kind = torch.float32, scale_blocks(K), _kind(out, "out")
     _check(lib.moe_grouped_matmul_fp8(rows, N, K, groups, _need("a_q", a_q, (rows, K), _F8, dev),
                                       _need("a_scale", a_scale, (kb, rows), f32, dev),
                                       _need("offsets", offsets, (groups + 1,), torch.int32, dev),
@@ -486,7 +510,7 @@ def moe_grouped_matmul_fp8(a_q, a_scale, offsets, b_q, b_scale, out, ws, stream=
 def moe_expert_ffn_fp8(cfg, x_q, x_scale, offsets, w1_q, w1_scale, w2_q, w2_scale, h_q, h_scale,
                        y_perm, ws, stream=None):
     """moe_expert_ffn on e4m3 rows and weights; h in e4m3 too, y_perm fp32."""
-    n, d, f, E, dev = cfg.T * cfg.k, cfg.d_model, cfg.d_ff, cfg.E, torch.cuda.current_device()
+    n, d, f, E, dev = cfg.T * cfg.k, cfg.d_model, cfg.d_ff, cfg.E, _here("x_q", x_q)
     f32, db, fb = torch.float32, scale_blocks(d), scale_blocks(f)
     _check(lib.moe_expert_ffn_fp8(ctypes.byref(cfg), _need("x_q", x_q, (n, d), _F8, dev),
                                   _need("x_scale", x_scale, (db, n), f32, dev),
@@ -538,7 +562,66 @@ class MoELayer:
         return self.y
 
 
-__all__ = ["ACT", "DEVERR", "DTYPE", "GATING", "MoEConfig", "MoEError", "MoELayer", "STATUS", "lib",
+class MoELayerFP8:
+    """One layer configuration behind its norm, with the experts in 8 bits, for inference.
+
+    forward(x, residual) takes r = x + residual, n = rmsnorm(r) when weights hold "norm", else
+    n = x; routes the 16-bit n as MoELayer does and runs the experts on n in e4m3 with e4m3
+    weights.  weights: as for MoELayer, with norm [d] bf16 or without; w1 and w2 in bf16 (they
+    are quantised here, once), or (q, scale) pairs as quantize_weights gives them.
+    """
+
+    def __init__(self, cfg: MoEConfig, weights: dict, eps: float = 1e-6, device="cuda"):
+        if cfg.dtype != DTYPE["bf16"] or cfg.hidden_f16:
+            raise MoEError(2, "8-bit experts belong to bf16 layers without hidden_f16")
+        self.cfg, self.eps = cfg, eps
+        T, k, E, d, f = cfg.T, cfg.k, cfg.E, cfg.d_model, cfg.d_ff
+        n, db, fb = T * k, scale_blocks(d), scale_blocks(f)
+        self.w = {name: weights.get(name) for name in ("w_gate", "w_noise", "logit_bias", "norm")}
+        for name in ("w1", "w2"):
+            w = weights[name]
+            self.w[name] = w if isinstance(w, tuple) else quantize_weights(w)
+        new = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device=device)  # noqa: E731
+        bf16, i32 = torch.bfloat16, torch.int32
+        normed = self.w["norm"] is not None
+        self.residual = new(T, d, t=bf16) if normed else None  # r of the last forward
+        self.n = new(T, d, t=bf16) if normed else None
+        self.n_q, self.n_scale = new(T, d, t=_F8), new(db, T)
+        self.topk_idx, self.topk_gate = new(T, k, t=i32), new(T, k)
+        self.counts, self.offsets = new(E, t=i32), new(E + 1, t=i32)
+        self.perm_src, self.slot_pos = new(n, t=i32), new(n, t=i32)
+        self.x_perm, self.x_perm_scale = new(n, d, t=_F8), new(db, n)
+        self.h, self.h_scale = new(n, f, t=_F8), new(fb, n)
+        self.y_perm = new(n, d)
+        self.y = new(T, d, t=bf16 if cfg.y_bf16 else torch.float32)
+        self.ws = workspace(cfg, device)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                noise: Optional[torch.Tensor] = None, stream=None):
+        """y [T, d] of x [T, d] bf16; the sum with the residual is kept in self.residual."""
+        cfg, w, ws = self.cfg, self.w, self.ws
+        if w["norm"] is not None:
+            moe_rmsnorm(x, w["norm"], self.eps, residual=residual, residual_out=self.residual,
+                        y=self.n, y_q=self.n_q, y_scale=self.n_scale, stream=stream)
+            rows = self.n
+        elif residual is not None:
+            raise ValueError("a residual is added by the norm: weights hold none")
+        else:
+            moe_quantize_rows_fp8(x, self.n_q, self.n_scale, stream=stream)
+            rows = x
+        moe_route(cfg, rows, w["w_gate"], self.topk_idx, self.topk_gate, ws, w_noise=w["w_noise"],
+                  noise=noise, logit_bias=w["logit_bias"], stream=stream)
+        moe_permute(cfg, self.topk_idx, None, self.counts, self.offsets, self.perm_src,
+                    self.slot_pos, None, ws, stream=stream)
+        moe_gather_rows_fp8(cfg, self.n_q, self.n_scale, self.perm_src, self.offsets, self.x_perm,
+                            self.x_perm_scale, ws, stream=stream)
+        moe_expert_ffn_fp8(cfg, self.x_perm, self.x_perm_scale, self.offsets, *w["w1"], *w["w2"],
+                           self.h, self.h_scale, self.y_perm, ws, stream=stream)
+        moe_combine(cfg, self.y_perm, self.slot_pos, self.topk_gate, self.y, ws, stream=stream)
+        return self.y
+
+
+__all__ = ["MoELayerFP8", "ACT", "DEVERR", "DTYPE", "GATING", "MoEConfig", "MoEError", "MoELayer", "STATUS", "lib",
            "make_config", "moe_capacity", "moe_combine", "moe_expert_ffn", "moe_forward",
            "moe_forward_workspace_size", "moe_get_error", "moe_permute", "moe_route",
            "moe_workspace_size", "workspace", "last_launch_count", "moe_bf16_to_f16",

@@ -107,7 +107,10 @@ def test_quantize_weights(shape, dtype):
 
 SHAPES = [(1, 8, 16), (1, 128, 128), (1, 1024, 8192), (3, 136, 144), (17, 4096, 1024), (127, 256, 128),
           (128, 256, 256), (129, 264, 272), (300, 520, 1040), (33, 1000, 2064), (257, 384, 4096),
-          (513, 1024, 512), (1025, 768, 768)]
+          (513, 1024, 512), (1025, 768, 768),
+          # CTA pairs (ragged rows, columns and depth); 32-row tiles of 256 columns; many blocks
+          (4101, 1288, 272), (9000, 256, 400), (4096, 1280, 1024), (20, 19208, 144), (32, 20480, 128),
+          (70, 136, 20000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -179,12 +182,15 @@ GROUPS = {
     "single": [77],
     "pairs_of_tiles": [700, 600, 513, 511],
     "many": [(7 * i) % 5 for i in range(200)],
+    "medium": [100 - i for i in range(40)],
+    "large": [2300, 1, 0, 2100],
+    "large_and_empty": [0, 5000, 0, 255, 257],
 }
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("N,K", [(264, 272), (1024, 512)])
-@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("name,N,K", [(g, *nk) for g in GROUPS for nk in ((264, 272), (1024, 512), (5128, 144))
+                                      if nk[0] * len(GROUPS[g]) < 200_000])
 def test_grouped_matmul(name, N, K, dtype):
     """Rows in front of the first group and behind the last hold NaN bytes and scales, and
     their output rows keep what was there."""
@@ -242,6 +248,9 @@ EXPERTS = {  # T, d, f, E, k, act, capacity factor, skew
     "drops": (500, 128, 192, 6, 2, "gelu", 0.7, 0.3),
     "skewed": (1500, 256, 512, 8, 2, "relu", None, 1.0),
     "large_groups": (2100, 256, 640, 2, 2, "gelu", None, 0.0),
+    "pairs_gelu": (3000, 1024, 1344, 4, 2, "gelu", None, 0.3),
+    "pairs_relu_drops": (5000, 256, 4160, 3, 1, "relu", 0.9, 0.5),
+    "few_rows": (40, 256, 1088, 32, 1, "gelu", None, 0.1),
 }
 
 
@@ -306,3 +315,117 @@ def test_gather_bad_indices():
     moe.moe_gather_rows_fp8(cfg, x, xs, r["perm_src"], off, xp, xsp, r["ws"])
     assert moe.moe_get_error(r["ws"]) == moe.DEVERR["offsets"]
     assert torch.equal(xp.view(torch.uint8), before.view(torch.uint8))
+
+
+# ------------------------------------------------ streams, graphs, sizes, refusals
+
+def product_case(seed, M=300, N=520, K=1040):
+    a, sa = quantised_rows(rows(seed, M, K))
+    b, sb = (t[0] for t in weights(seed + 1, 1, N, K))
+    return a, sa, b, sb
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 8192), (300, 520, 1040), (4101, 1288, 272)])
+def test_same_bits_every_time_and_on_any_stream(M, N, K):
+    args = product_case(7, M, N, K)
+    ws = new_ws()
+    first = torch.empty(M, N, device="cuda")
+    moe.moe_matmul_fp8(*args, first, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(20):
+        out = torch.full_like(first, -7.0)
+        torch.cuda.synchronize()
+        moe.moe_matmul_fp8(*args, out, ws, stream=side if i % 2 else None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    assert moe.moe_get_error(ws) == 0
+
+
+def test_captured_graphs_share_a_workspace():
+    """Two graphs on one workspace, replayed in turn on one stream with new inputs, give what
+    eager calls give."""
+    ws = new_ws()
+    cases = [product_case(3), product_case(5, 4101, 1288, 272), product_case(9, 2, 256, 4096)]
+    outs = [torch.empty(c[0].shape[0], c[2].shape[0], device="cuda") for c in cases]
+    for c, o in zip(cases, outs):
+        moe.moe_matmul_fp8(*c, o, ws)   # first calls set kernel attributes
+    torch.cuda.synchronize()
+    graphs = []
+    for c, o in zip(cases, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_matmul_fp8(*c, o, ws)
+        graphs.append(g)
+    for seed in (21, 22):
+        want = []
+        for c in cases:
+            M, K = c[0].shape
+            q, s = quantised_rows(rows(seed, M, K))
+            c[0].copy_(q)
+            c[1].copy_(s)
+            want.append(torch.empty(M, c[2].shape[0], device="cuda"))
+            moe.moe_matmul_fp8(*c, want[-1], ws)
+        for o in outs:
+            o.fill_(-7.0)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert moe.moe_get_error(ws) == 0
+
+
+def test_output_past_2_31_elements():
+    M, N, K = 140_000, 16_384, 16
+    a, sa = quantised_rows(rows(1, M, K))
+    b, sb = (t[0] for t in weights(2, 1, N, K))
+    out, ws = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), new_ws()
+    moe.moe_matmul_fp8(a, sa, b, sb, out, ws)
+    bv = lo.weights_value(f64(b), f64(sb))
+    for r in (0, 65_536, 131_071, 131_072, M - 1):
+        av = lo.rows_value(f64(a[r:r + 1]), f64(sa[:, r:r + 1]))
+        want, mag = lo.grouped_matmul(av, [0, 1], bv[None])
+        assert (np.abs(f64(out[r:r + 1]) - want) <= product_tol(mag, want, K, torch.bfloat16)).all()
+    assert moe.moe_get_error(ws) == 0
+
+
+def test_no_rows():
+    ws = new_ws()
+    e8, e = torch.empty(0, 128, device="cuda").to(F8), torch.empty(1, 0, device="cuda")
+    b, sb = weights(1, 2, 128, 128)
+    out = torch.empty(0, 128, device="cuda")
+    moe.moe_matmul_fp8(e8, e, b[0], sb[0], out, ws)
+    moe.moe_grouped_matmul_fp8(e8, e, torch.zeros(3, dtype=torch.int32, device="cuda"), b, sb, out, ws)
+    moe.moe_quantize_rows_fp8(torch.empty(0, 128, device="cuda"), e8, e)
+    assert moe.last_launch_count() == 0
+
+
+def test_refusals():
+    a, sa, b, sb = product_case(1, 32, 64, 128)
+    out, ws = torch.empty(32, 64, device="cuda"), new_ws()
+    call = moe.moe_matmul_fp8
+    with pytest.raises(ValueError):
+        call(a.float(), sa, b, sb, out, ws)                      # type
+    with pytest.raises(ValueError):
+        call(a, sa.t().contiguous(), b, sb, out, ws)             # scales of another layout
+    with pytest.raises(ValueError):
+        call(a, sa, b, sb, torch.empty(64, 32, device="cuda").t(), ws)   # strides
+    with pytest.raises(ValueError):
+        call(a, sa, b, sb, out.half(), ws)
+    with pytest.raises(ValueError):
+        call(a, sa.cpu(), b, sb, out, ws)
+    with pytest.raises(ValueError):
+        call(a, sa, b, sb, out, ws[:128])                        # workspace too small
+    with pytest.raises(TypeError):
+        call(a, sa, b, sb, None, ws)
+    with pytest.raises(TypeError):
+        call(a, sa, b, sb, out, None)
+    q = torch.empty(32, 24, dtype=F8, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.moe_quantize_rows_fp8(torch.zeros(32, 24, device="cuda"), q, torch.empty(1, 32, device="cuda"))
+    with pytest.raises(ValueError):
+        moe.moe_rmsnorm(torch.zeros(4, 64, device="cuda"), torch.ones(32, device="cuda"),
+                        y=torch.empty(4, 64, device="cuda"))
+    with pytest.raises(moe.MoEError):
+        moe.MoELayerFP8(moe.make_config(8, 64, 64, 4, 1, hidden_f16=True), {})

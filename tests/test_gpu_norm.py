@@ -139,3 +139,59 @@ def test_backward_of_no_rows():
     moe.moe_rmsnorm_backward(e, dw.clone(), torch.empty(0, device="cuda"), e, e,
                              torch.empty(256, dtype=torch.uint8, device="cuda"), dweight=dw)
     assert not dw.any()
+
+
+def test_rows_past_2_31_elements():
+    rows, d = 140_000, 16_384
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(1))
+    w = draw(2, 1, d, torch.bfloat16)[0]
+    y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+    moe.moe_rmsnorm(x, w, y=y, rstd=rstd)
+    for r in (0, 131_071, 131_072, rows - 1):
+        want, wr = lo.rmsnorm(f64(x[r:r + 1]), f64(w), 1e-6)
+        assert abs(f64(rstd[r:r + 1]) - wr) <= 32 * U * wr
+        assert (np.abs(f64(y[r:r + 1]) - want) <= (36 * U + HALF[torch.bfloat16] * (1 + 36 * U)) * np.abs(want)).all()
+
+
+def test_captured_and_on_another_stream():
+    """Forward and backward captured into one graph and replayed on new inputs equal the eager
+    calls, as do calls on a side stream."""
+    rows, d = 1500, 768
+    x, res, w = draw(1, rows, d, torch.bfloat16), draw(2, rows, d, torch.bfloat16), draw(3, 1, d, torch.bfloat16)[0]
+    dy = draw(4, rows, d, torch.float32)
+    f32 = dict(dtype=torch.float32, device="cuda")
+    ws = moe.rmsnorm_backward_workspace(rows, d)
+
+    def outputs():
+        return {"r": torch.empty_like(x), "y": torch.empty_like(x), "q": torch.empty(rows, d, dtype=F8, device="cuda"),
+                "s": torch.empty(moe.scale_blocks(d), rows, **f32), "rstd": torch.empty(rows, **f32),
+                "dx": torch.empty(rows, d, **f32), "dw": torch.empty(d, **f32)}
+
+    def step(o, stream=None):
+        moe.moe_rmsnorm(x, w, residual=res, residual_out=o["r"], y=o["y"], y_q=o["q"], y_scale=o["s"], rstd=o["rstd"],
+                        stream=stream)
+        moe.moe_rmsnorm_backward(o["r"], w, o["rstd"], dy, o["dx"], ws, dresidual=dy, dweight=o["dw"], stream=stream)
+
+    o = outputs()
+    step(o)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(o)
+    side = torch.cuda.Stream()
+    for seed in (11, 12):
+        x.copy_(draw(seed, rows, d, torch.bfloat16))
+        want = outputs()
+        step(want)
+        torch.cuda.synchronize()
+        for k in o:
+            o[k].view(torch.uint8).zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        other = outputs()
+        torch.cuda.synchronize()
+        step(other, stream=side)
+        torch.cuda.synchronize()
+        for k in o:
+            assert torch.equal(o[k].view(torch.uint8), want[k].view(torch.uint8)), k
+            assert torch.equal(other[k].view(torch.uint8), want[k].view(torch.uint8)), k
