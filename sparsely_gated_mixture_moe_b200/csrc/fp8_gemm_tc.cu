@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int THREADS = 128 + EPI_WARPS * 32;
   static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + STAGING +
                                     256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
-                                    4 * (MAX_GROUPS + 1 + 40);
+                                    4 * (2 * (MAX_GROUPS + 1) + 40);
   static_assert(STAGE_BYTES >= BM * BK, "the MMA's 128 rows stay in the stage");
   static_assert(MODE != kSplit || BN == CW, "one 128-column block a tile");
   static_assert(MODE != kSplit || EPI_WARPS * 32 * CW * 4 <= RING_BYTES, "partial sums fit the ring");
@@ -100,28 +100,27 @@ struct Tile {
   int valid;
 };
 
-__device__ __forceinline__ Tile decode_tile(int L, const int* tp, const Args& a, int bm) {
+// tp: tiles of rows in front of each group; starts: the groups' offsets.  Both in shared memory:
+// from global memory two dependent loads held every warp up for 1,000 clocks a tile.
+__device__ __forceinline__ Tile decode_tile(int L, const int* tp, const int* starts, const Args& a, int bm) {
   Tile t;
+  const int mt = L / a.n_tiles;
+  t.nt = L - mt * a.n_tiles;
   if (a.offsets == nullptr) {
     t.g = 0;
-    const int mt = L / a.n_tiles;
-    t.nt = L - mt * a.n_tiles;
     t.row0 = static_cast<int64_t>(mt) * bm;
     t.valid = static_cast<int>(min(static_cast<int64_t>(bm), a.rows - t.row0));
     return t;
   }
-  int lo = 0, hi = a.groups - 1;  // the largest g with tp[g] * n_tiles <= L
+  int lo = 0, hi = a.groups - 1;  // the largest g with tp[g] <= mt
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(tp[mid]) * a.n_tiles <= L) lo = mid; else hi = mid - 1;
+    if (tp[mid] <= mt) lo = mid; else hi = mid - 1;
   }
   t.g = lo;
-  const int local = L - tp[lo] * a.n_tiles;
-  const int mt = local / a.n_tiles;
-  t.nt = local - mt * a.n_tiles;
-  const int r0 = __ldg(a.offsets + lo), r1 = __ldg(a.offsets + lo + 1);
-  t.row0 = r0 + mt * bm;
-  t.valid = min(bm, r1 - static_cast<int>(t.row0));
+  const int row0 = starts[lo] + (mt - tp[lo]) * bm;
+  t.row0 = row0;
+  t.valid = min(bm, starts[lo + 1] - row0);
   return t;
 }
 
@@ -365,6 +364,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
   float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [2 BUFS][BN / 128][128 rows]
   int* scratch = reinterpret_cast<int*>(scales + SCALE_FLOATS);
   int* tp = scratch + 40;
+  int* starts = tp + MAX_GROUPS + 1;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
   grid_dep_launch();
   int tiles;
   if (a.offsets != nullptr) {
+    for (int g = threadIdx.x; g <= a.groups; g += blockDim.x) starts[g] = a.offsets[g];
     const bool ok = block_tile_prefix(a.offsets, a.groups, a.rows, C::TBM, tp, scratch);
     if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_error(a.err, kErrOffsets);
     tiles = ok ? tp[a.groups] * a.n_tiles : 0;
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool aborted = false;
       for (int L = first; L < tiles && !aborted; L += step) {
-        const Tile t = decode_tile(L, tp, a, C::TBM);
+        const Tile t = decode_tile(L, tp, starts, a, C::TBM);
         const int brow = t.g * a.N + t.nt * BN + rank * C::B_ROWS;
         const int arow = static_cast<int>(t.row0) + rank * ROWS;
         const int boxes = a_boxes<C::A_BOX>(t.valid - rank * ROWS);
@@ -565,13 +566,13 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
       uint32_t buf_phase = 1;  // a barrier's first turn: nothing to wait for
       bool aborted = false;
       Ahead next;
-      if (first < tiles) load(next, decode_tile(first, tp, a, C::TBM), kb_lo);
+      if (first < tiles) load(next, decode_tile(first, tp, starts, a, C::TBM), kb_lo);
       for (int L = first; L < tiles && !aborted; L += step) {
-        const Tile t = decode_tile(L, tp, a, C::TBM);
+        const Tile t = decode_tile(L, tp, starts, a, C::TBM);
         for (int kb0 = kb_lo; kb0 < kb_hi && !aborted; kb0 += GROUP) {
           const Ahead v = next;
           if (kb0 + GROUP < kb_hi) load(next, t, kb0 + GROUP);
-          else if (L + step < tiles) load(next, decode_tile(L + step, tp, a, C::TBM), kb_lo);
+          else if (L + step < tiles) load(next, decode_tile(L + step, tp, starts, a, C::TBM), kb_lo);
 #pragma unroll
           for (int i = 0; i < GROUP; ++i) {
             if (kb0 + i >= kb_hi) break;
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     uint32_t buf_phase = 0;
     bool aborted = false;
     for (int L = first; L < tiles && !aborted; L += step) {
-      const Tile t = decode_tile(L, tp, a, C::TBM);
+      const Tile t = decode_tile(L, tp, starts, a, C::TBM);
       const int valid = t.valid - rank * ROWS;
       const bool row_ok = r < valid, warp_ok = quarter * 32 < valid;
       float acc[CW];
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     __syncwarp();
     cluster_sync_all();
     if (warp >= 4 && first < tiles) {
-      const Tile t = decode_tile(first, tp, a, C::TBM);
+      const Tile t = decode_tile(first, tp, starts, a, C::TBM);
       const int j0 = CW / 4 * part / share, width = CW / 4 / share;  // four columns each
       // a thread for four columns of a row, all loads of the cluster's sums in flight at once
       for (int i = threadIdx.x - 128; i < t.valid * width; i += C::EPI_WARPS * 32) {
