@@ -34,10 +34,13 @@ moe_status nothing_to_do() {
   return MOE_OK;
 }
 
+// Longest row or contraction: block counts and coordinates are 32-bit.
+constexpr int64_t kMaxWidth = int64_t{1} << 30;
+
 // rows and columns of a matrix whose rows are read in vectors of `step` values
 moe_status check_rows(int64_t rows, int64_t d, int step) {
   if (rows < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
-  if (rows >= (int64_t{1} << 31) || d % step != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows >= (int64_t{1} << 31) || d > kMaxWidth || d % step != 0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -58,7 +61,7 @@ moe_status check_product(int64_t rows, int32_t N, int32_t K, int64_t groups, int
   if (rows < 0 || N <= 0 || K <= 0 || groups <= 0) return MOE_ERR_INVALID_ARG;
   const moe_status st = check_dtype(out_dtype);
   if (st != MOE_OK) return st;
-  if (N % 8 != 0 || K % 16 != 0 || groups > 1024) return MOE_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || K % 16 != 0 || K > kMaxWidth || groups > 1024) return MOE_ERR_UNSUPPORTED;
   // rows and weight rows are 32-bit TMA coordinates, tiles are counted in 32 bits
   if (rows >= (int64_t{1} << 31) - 256 || groups * N >= (int64_t{1} << 31) - 256)
     return MOE_ERR_UNSUPPORTED;
@@ -161,7 +164,8 @@ moe_status moe_quantize_weights_fp8(int64_t groups, int32_t N, int32_t K, int32_
   if (groups < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   const moe_status st = check_dtype(dtype);
   if (st != MOE_OK) return st;
-  if (K % 16 != 0 || groups > INT_MAX / (blocks_of(N) * blocks_of(K))) return MOE_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || N > kMaxWidth || K > kMaxWidth || groups > INT_MAX / (blocks_of(N) * blocks_of(K)))
+    return MOE_ERR_UNSUPPORTED;
   if (groups == 0) return nothing_to_do();
   if (!w || !q || !scale || !aligned16(w) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   Entry en(nullptr, stream);

@@ -39,6 +39,7 @@ namespace f8 {
 
 constexpr int BM = 128;
 constexpr int BK = 128;  // bytes of a k-block's rows: one scale block of the contraction
+constexpr int A_BYTES = BM * BK;
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr int CW = 128;    // most columns of an epilogue thread: a scale block
@@ -51,29 +52,26 @@ constexpr int kFewRows = 8;
 enum { kSingle = 0, kPair = 1, kSplit = 2 };
 constexpr int kMaxSplits = 8;
 
-// BN columns a tile; ROWS of A a CTA holds: 128, or 32 for few rows a group, whose weights then
-// have most of the ring.  The MMA's other 96 rows are whatever follows in the stage.
-template <int BN, int MODE, int ROWS>
+// BN columns a tile.
+template <int BN, int MODE>
 struct Cfg {
   static constexpr bool PAIR = MODE == kPair;
-  static constexpr int TBM = PAIR ? 2 * ROWS : ROWS;       // rows of a tile
-  static constexpr int A_BYTES = ROWS * BK;
+  static constexpr int TBM = PAIR ? 2 * BM : BM;           // rows of a tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // weight rows a CTA loads
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
-  static constexpr int STAGES = ROWS == 32 ? (BN == 256 ? 5 : 8) : !PAIR && BN == 256 ? 3 : 4;
+  static constexpr int STAGES = !PAIR && BN == 256 ? 3 : 4;
   static constexpr int BUFS = TMEM_COLS / BN;              // accumulators: 2 or 4
   static constexpr int TURN = STAGES % BUFS == 0 ? STAGES : STAGES * BUFS;  // of stages and accumulators
-  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 to 180 KB
-  static constexpr int A_BOX = PAIR ? ROWS : 32;           // rows of A in one copy: ragged tiles need few
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // 128 or 144 KB
+  static constexpr int A_BOX = PAIR ? BM : 32;             // rows of A in one copy: ragged tiles need few
   static constexpr int EPI_WARPS = BN / CW * 4;            // 8 or 4
   // bytes of output a warp stages: 32 rows of 512 (all columns as fp32), or of 256 at a time
   static constexpr int STAGED = 32 * (BN == 128 ? 512 : 256);
-  static constexpr int STAGING = BN / CW * (ROWS == 32 ? kFewRows * CW * 4 : 4 * STAGED);
+  static constexpr int STAGING = EPI_WARPS * STAGED;
   static constexpr int THREADS = 128 + EPI_WARPS * 32;
   static constexpr int SMEM_BYTES = 1024 /*align slack*/ + RING_BYTES + STAGING +
                                     256 /*barriers, flags*/ + SCALE_FLOATS * 4 +
                                     4 * (2 * (MAX_GROUPS + 1) + 40);
-  static_assert(STAGE_BYTES >= BM * BK, "the MMA's 128 rows stay in the stage");
   static_assert(MODE != kSplit || BN == CW, "one 128-column block a tile");
   static_assert(MODE != kSplit || EPI_WARPS * 32 * CW * 4 <= RING_BYTES, "partial sums fit the ring");
   static_assert(2 * STAGES + 2 * BUFS + 2 <= 32, "barriers and flags fit 256 bytes");
@@ -340,14 +338,14 @@ __device__ __forceinline__ void put_few_e4m3(const Args& a, uint8_t* to, int lan
   __syncwarp();  // read before the next tile's rows are written
 }
 
-template <int BN, int OUT, int MODE, int ROWS>
-__global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
+template <int BN, int OUT, int MODE>
+__global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
     fp8_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmO, const Args a) {
-  using C = Cfg<BN, MODE, ROWS>;
+  using C = Cfg<BN, MODE>;
   constexpr bool PAIR = C::PAIR;
-  constexpr int A_BYTES = C::A_BYTES, BUFS = C::BUFS;
+  constexpr int BUFS = C::BUFS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -428,8 +426,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
       for (int L = first; L < tiles && !aborted; L += step) {
         const Tile t = decode_tile(L, tp, starts, a, C::TBM);
         const int brow = t.g * a.N + t.nt * BN + rank * C::B_ROWS;
-        const int arow = static_cast<int>(t.row0) + rank * ROWS;
-        const int boxes = a_boxes<C::A_BOX>(t.valid - rank * ROWS);
+        const int arow = static_cast<int>(t.row0) + rank * BM;
+        const int boxes = a_boxes<C::A_BOX>(t.valid - rank * BM);
         // a pair's copies all complete on the barrier of rank 0
         const uint32_t tx = static_cast<uint32_t>(
             (PAIR ? a_boxes<C::A_BOX>(t.valid) + a_boxes<C::A_BOX>(t.valid - BM) : boxes) * C::A_BOX * BK +
@@ -540,18 +538,18 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
       // ------------------------------------------------------------ scales
       // GROUP blocks at a time: the next group's loads are in flight while this one's wait
       // for their accumulators.
-      constexpr int GROUP = 4, HALVES = BN / CW, ROW4 = ROWS / 32;
+      constexpr int GROUP = 4, HALVES = BN / CW;
       struct Ahead {
-        float a[GROUP][ROW4], b[GROUP][HALVES];
+        float a[GROUP][4], b[GROUP][HALVES];
       };
       auto load = [&](Ahead& v, const Tile& t, int kb0) {
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
           const int kb = min(kb0 + i, kb_hi - 1);
 #pragma unroll
-          for (int j = 0; j < ROW4; ++j)
+          for (int j = 0; j < 4; ++j)
             v.a[i][j] = __ldg(a.a_scale + static_cast<int64_t>(kb) * a.rows + t.row0 +
-                              min(rank * ROWS + lane + 32 * j, t.valid - 1));
+                              min(rank * BM + lane + 32 * j, t.valid - 1));
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
             const int nb = min(t.nt * HALVES + h, a.nblocks - 1);
@@ -584,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
 #pragma unroll
             for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-              for (int j = 0; j < ROW4; ++j) to[h * BM + 32 * j] = v.a[i][j] * v.b[i][h];
+              for (int j = 0; j < 4; ++j) to[h * BM + 32 * j] = v.a[i][j] * v.b[i][h];
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull0 + 8 * buf);
             if (++slot == 2 * BUFS) slot = 0;
@@ -610,13 +608,12 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
     const float* my_scale = scales + cg * BM + r;
     const uint32_t free0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
     const uint32_t to = smem_u32(staging) + (warp - 4) * C::STAGED;
-    uint8_t* few_at = staging + (ROWS == 32 ? cg * kFewRows * CW * 4 : (warp - 4) * C::STAGED);
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool aborted = false;
     for (int L = first; L < tiles && !aborted; L += step) {
       const Tile t = decode_tile(L, tp, starts, a, C::TBM);
-      const int valid = t.valid - rank * ROWS;
+      const int valid = t.valid - rank * BM;
       const bool row_ok = r < valid, warp_ok = quarter * 32 < valid;
       float acc[CW];
 #pragma unroll
@@ -674,13 +671,13 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
         continue;
       }
       const int n = min(CW, a.N - col);
-      const int row0 = static_cast<int>(t.row0) + rank * ROWS + quarter * 32;  // the warp's first
+      const int row0 = static_cast<int>(t.row0) + rank * BM + quarter * 32;  // the warp's first
       const int64_t row = row0 + lane, at = row * a.N + col;
-      const bool whole = ROWS == BM && valid >= quarter * 32 + 32;  // else there is no room to stage
+      const bool whole = valid >= quarter * 32 + 32;
       if constexpr (OUT == kFp8OutE4m3) {
         const int few = min(32, valid - quarter * 32);
         if (few <= kFewRows) {
-          put_few_e4m3(a, few_at, lane, acc, few, n, row0, col);
+          put_few_e4m3(a, staging + (warp - 4) * C::STAGED, lane, acc, few, n, row0, col);
           continue;
         }
         const float m = a.act == 2 ? activate<2>(acc, n) : activate<1>(acc, n);
@@ -750,9 +747,15 @@ __global__ void __launch_bounds__(Cfg<BN, MODE, ROWS>::THREADS, 1)
 
 }  // namespace f8
 
-// Groups of at least this many rows on average run on CTA pairs.
-constexpr int64_t kFp8PairMinRows = 256;
-// Groups of at most this many on average have tiles of 32 rows.
+// Groups of at least this many rows on average run on CTA pairs.  Products 1024 deep and 4096 wide:
+// 153 us on pairs against 172 for 16384 rows in one group (8192 wide), 170 against 186 for 16
+// groups averaging 2048; but 271 against 274 for 32 of 1024, 149 against 139 for 32 of 512 and 86
+// against 75 for 32 of 256, whose last 256-row tiles are half empty.
+constexpr int64_t kFp8PairMinRows = 1024;
+// Groups of at most this many on average stream their weights: tiles of 256 columns as long as they
+// occupy half of the SMs (32 rows in 64 groups, 4096 deep and 1024 wide: 26.3 us against 29.9
+// with 128 columns); products with more rows only where they occupy all (1024 x 2048 x 2048: 13.1
+// against 10.2).
 constexpr int64_t kFp8FewRows = 16;
 
 // Upper bound of a product's tiles of bm x bn: sum over groups of ceil(rows / bm), times n-tiles.
@@ -762,10 +765,10 @@ static int64_t max_tiles(const Fp8GemmProblem& p, int bm, int bn) {
   return mt * ((p.N + bn - 1) / bn);
 }
 
-template <int BN, int OUT, int MODE, int ROWS>
+template <int BN, int OUT, int MODE>
 static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const LaunchCtx& c) {
-  using C = f8::Cfg<BN, MODE, ROWS>;
-  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, MODE, ROWS>;
+  using C = f8::Cfg<BN, MODE>;
+  const auto kernel = f8::fp8_gemm_tc_kernel<BN, OUT, MODE>;
   constexpr int esize = OUT == kFp8OutF32 ? 4 : OUT == kFp8OutBf16 ? 2 : 1;
   CUtensorMap tmA, tmB, tmO;
   if (!make_tmap_1b(&tmA, p.a, static_cast<uint64_t>(p.rows), p.K, C::A_BOX) ||
@@ -789,11 +792,11 @@ static cudaError_t launch_tiles(const Fp8GemmProblem& p, f8::Args a, const Launc
                        C::SMEM_BYTES, c, tmA, tmB, tmO, a);
 }
 
-template <int BN, int MODE, int ROWS>
+template <int BN, int MODE>
 static cudaError_t launch_out(const Fp8GemmProblem& p, const f8::Args& a, const LaunchCtx& c) {
-  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, MODE, ROWS>(p, a, c);
-  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, MODE, ROWS>(p, a, c);
-  return launch_tiles<BN, kFp8OutE4m3, MODE, ROWS>(p, a, c);
+  if (p.out_type == kFp8OutBf16) return launch_tiles<BN, kFp8OutBf16, MODE>(p, a, c);
+  if (p.out_type == kFp8OutF32) return launch_tiles<BN, kFp8OutF32, MODE>(p, a, c);
+  return launch_tiles<BN, kFp8OutE4m3, MODE>(p, a, c);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
@@ -815,29 +818,22 @@ cudaError_t launch_fp8_gemm(const Fp8GemmProblem& p, const LaunchCtx& c) {
   a.vec32 = row_bytes % 32 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
   a.err = c.err;
   a.splits = 1;
-  // Pairs for groups that fill their tiles, as long as the pairs fill the device; then the
-  // widest tile that does; below that tiles of 128 columns, and clusters that split the
-  // contraction among as many CTAs as there are SMs for, two blocks each at least (an e4m3
-  // output needs all sums of a block of columns in one thread and is not split).
+  // Pairs for large groups, as long as the pairs fill the device; then the widest tile that
+  // does; below that tiles of 128 columns, and clusters that split the contraction among as
+  // many CTAs as there are SMs for, two blocks each at least (1 x 1024 x 8192: 8.6 us in eight,
+  // 19.8 in one; an e4m3 output needs all sums of a block of columns in one thread and is not
+  // split).
   if (p.rows >= kFp8PairMinRows * p.groups && 2 * max_tiles(p, 2 * f8::BM, 256) >= c.num_sms)
-    return launch_out<256, f8::kPair, f8::BM>(p, a, c);
-  // Tiles of 32 rows, whose weights have 144 to 160 KB of shared memory on their way instead of
-  // 64 to 96, for groups that mostly fit in one.
-  const bool few = p.offsets == nullptr ? p.rows <= 32 : p.rows <= kFp8FewRows * p.groups;
-  const int bm = few ? 32 : f8::BM;
-  if (max_tiles(p, bm, 256) >= (few ? c.num_sms / 2 : c.num_sms))
-    return few ? launch_out<256, f8::kSingle, 32>(p, a, c) : launch_out<256, f8::kSingle, f8::BM>(p, a, c);
-  const int64_t tiles = max_tiles(p, bm, 128);
+    return launch_out<256, f8::kPair>(p, a, c);
+  const bool few = p.rows <= kFp8FewRows * p.groups;
+  if (max_tiles(p, f8::BM, 256) >= (few ? c.num_sms / 2 : c.num_sms)) return launch_out<256, f8::kSingle>(p, a, c);
+  const int64_t tiles = max_tiles(p, f8::BM, 128);
   if (p.out_type != kFp8OutE4m3)
     while (a.splits < f8::kMaxSplits && tiles * a.splits * 2 <= c.num_sms && a.kblocks >= a.splits * 4)
       a.splits *= 2;
-  if (a.splits == 1)
-    return few ? launch_out<128, f8::kSingle, 32>(p, a, c) : launch_out<128, f8::kSingle, f8::BM>(p, a, c);
-  if (p.out_type == kFp8OutBf16)
-    return few ? launch_tiles<128, kFp8OutBf16, f8::kSplit, 32>(p, a, c)
-               : launch_tiles<128, kFp8OutBf16, f8::kSplit, f8::BM>(p, a, c);
-  return few ? launch_tiles<128, kFp8OutF32, f8::kSplit, 32>(p, a, c)
-             : launch_tiles<128, kFp8OutF32, f8::kSplit, f8::BM>(p, a, c);
+  if (a.splits == 1) return launch_out<128, f8::kSingle>(p, a, c);
+  return p.out_type == kFp8OutBf16 ? launch_tiles<128, kFp8OutBf16, f8::kSplit>(p, a, c)
+                                   : launch_tiles<128, kFp8OutF32, f8::kSplit>(p, a, c);
 }
 
 }  // namespace moe

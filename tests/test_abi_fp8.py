@@ -55,6 +55,8 @@ def test_quantisers():
     assert w(g=0) == 0
     assert w(g=-1) == 1 and w(n=0) == 1 and w(k=0) == 1 and w(t=-1) == 1 and w(k=24) == 2
     assert w(g=1 << 30, n=1024, k=1024) == 2
+    big = (1 << 30) + 16                                  # block counts are 32-bit
+    assert rows(d=big) == 2 and w(n=big) == 2 and w(k=big) == 2 and w(k=(1 << 31) - 16) == 2
     assert w(x=None) == 1 and w(q=ODD) == 1
 
 
@@ -70,7 +72,7 @@ def test_products():
     assert mm(M=0) == 0 and gm(rows=0) == 0
     for f in (mm, gm):
         assert f(N=0) == 1 and f(K=0) == 1 and f(t=2) == 1
-        assert f(N=60) == 2 and f(K=24) == 2
+        assert f(N=60) == 2 and f(K=24) == 2 and f(K=(1 << 30) + 16) == 2 and f(N=(1 << 31) - 8) == 2
         for k in ("a", "sa", "b", "sb", "out", "ws"):
             assert f(**{k: None}) == 1
         for k in ("a", "b", "out", "ws"):
