@@ -340,16 +340,18 @@ def _need(what: str, t, shape, dtype, device: int):
 
 
 def _here(what: str, t) -> int:
-    """The current device, where t must be."""
+    """The current device, where t must be.  (A CUDA tensor's existence means that CUDA is
+    initialised, which torch.cuda.current_device would check again.)"""
     try:
         device = t.get_device()
     except AttributeError:
         raise TypeError("%s must be a torch.Tensor" % what) from None
     if device < 0:
         raise ValueError("%s must be a CUDA tensor (libmoe has no CPU path)" % what)
-    if device != torch.cuda.current_device():
+    current = torch._C._cuda_getDevice()
+    if device != current:
         raise ValueError("%s is on device %d, the call runs on the current device %d"
-                         % (what, device, torch.cuda.current_device()))
+                         % (what, device, current))
     return device
 
 
