@@ -42,7 +42,7 @@ constexpr int BK = 128;  // bytes of a k-block's rows: one scale block of the co
 constexpr int A_BYTES = BM * BK;
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
-constexpr int CW = 128;    // most columns of an epilogue thread: a scale block
+constexpr int CW = 128;    // columns of an epilogue thread: a scale block
 constexpr int SCALE_FLOATS = 1024;  // slots of 2 BUFS blocks
 // A warp with at most this many rows spreads each row's scale block over its lanes (below).
 constexpr int kFewRows = 8;
@@ -129,7 +129,7 @@ __device__ __forceinline__ int a_boxes(int valid) {
 }
 
 // 2-D tiled bulk tensor store shared -> global (box as in the map, 128-byte swizzled rows of
-// 128 bytes; columns past the tensor's are not written), one commit group of the thread.
+// 128 bytes; columns past the tensor's are not written), part of the thread's next commit group.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(Cfg<BN, MODE>::THREADS, 1)
   int tiles;
   if (a.offsets != nullptr) {
     for (int g = threadIdx.x; g <= a.groups; g += blockDim.x) starts[g] = a.offsets[g];
-    const bool ok = block_tile_prefix(a.offsets, a.groups, a.rows, C::TBM, tp, scratch);
+    // the offsets are read from global memory once: a second round trip took half a microsecond
+    const bool ok = block_tile_prefix(starts, a.groups, a.rows, C::TBM, tp, scratch);
     if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_error(a.err, kErrOffsets);
     tiles = ok ? tp[a.groups] * a.n_tiles : 0;
   } else {

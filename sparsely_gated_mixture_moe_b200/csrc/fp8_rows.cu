@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = T * k, s0 = static_cast<int64_t>(blockIdx.x) * 32;
-  const int kept = *n_kept;
+  // the number of kept rows and the rows' sources in one round trip
+  const int kept = *n_kept, asg = s0 + lane < n ? perm_src[s0 + lane] : -1;
   if (kept < 0 || kept > n) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, kErrOffsets);
     return;
@@ -120,8 +121,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   if (warp == 0) {
     int t = -1;
     if (s0 + lane < kept) {
-      const int a = perm_src[s0 + lane];
-      if (a >= 0 && a < n) t = a / k;
+      if (asg >= 0 && asg < n) t = asg / k;
       else set_error(err, kErrSlot);  // not a permutation written by the permute step
     }
     src[lane] = t;
