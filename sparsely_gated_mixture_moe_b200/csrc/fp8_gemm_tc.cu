@@ -248,21 +248,20 @@ template <int ACT>
 __device__ __forceinline__ float activate(float (&acc)[CW], int n) {
   float m[4] = {kAmaxFloor, kAmaxFloor, kAmaxFloor, kAmaxFloor};  // four chains
 #pragma unroll
-  for (int c = 0; c < CW / 8; ++c) {
-    float v[8];
+  for (int c = 0; c < CW / 16; ++c) {  // sixteen values a step
+    float v[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = acc[c * 8 + j];
+    for (int j = 0; j < 16; ++j) v[j] = acc[c * 16 + j];
     if (ACT == 1) {
-      // fmaxf would turn a NaN into 0
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+      for (int j = 0; j < 16; ++j) v[j] = relu_nan(v[j]);
     } else {
-      gelu_poly<4>(v);
+      gelu_poly<8>(v);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[c * 8 + j] = c * 8 < n ? v[j] : 0.0f;
+    for (int j = 0; j < 16; ++j) acc[c * 16 + j] = c * 16 < n ? v[j] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = amax3_nan(m[j], acc[c * 8 + 2 * j], acc[c * 8 + 2 * j + 1]);
+    for (int j = 0; j < 8; ++j) m[j % 4] = amax3_nan(m[j % 4], acc[c * 16 + 2 * j], acc[c * 16 + 2 * j + 1]);
   }
   return amax3_nan(m[0], m[1], max_nan(m[2], m[3]));
 }
@@ -322,7 +321,7 @@ __device__ __forceinline__ void put_few_e4m3(const Args& a, uint8_t* to, int lan
       gelu_poly<2>(v);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+      for (int j = 0; j < 4; ++j) v[j] = relu_nan(v[j]);
     }
     const bool in = lane * 4 < n;
     float m = in ? amax3_nan(v[0], v[1], amax3_nan(v[2], v[3], kAmaxFloor)) : kAmaxFloor;
