@@ -195,3 +195,39 @@ def test_captured_and_on_another_stream():
         for k in o:
             assert torch.equal(o[k].view(torch.uint8), want[k].view(torch.uint8)), k
             assert torch.equal(other[k].view(torch.uint8), want[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,d", [(64, 1024), (33, 2576), (8, 8208)])
+def test_forward_ties_of_the_8_bit_output(rows, d, residual):
+    """For 16-bit r and w, 448 y / max|y| = 448 r w / max|r w| is a quotient of whole numbers
+    below 2^25 but for powers of two.  Where it is not midway between two e4m3 values it is at
+    least 2^-22 of itself away, more than an fp32 rounding; where it is midway, it is so
+    exactly.  So the output is the rounding to nearest even of the exact quotient, whatever
+    the row's rstd."""
+    x, w = draw(1, rows, d, torch.bfloat16), (1 + 0.1 * draw(2, 1, d, torch.float32)[0]).to(torch.bfloat16)
+    res = draw(3, rows, d, torch.bfloat16) if residual else None
+    s = torch.empty_like(x)
+    q, qs = torch.empty(rows, d, dtype=F8, device="cuda"), torch.empty(moe.scale_blocks(d), rows, device="cuda")
+    moe.moe_rmsnorm(x, w, 1e-5, residual=res, residual_out=s, y_q=q, y_scale=qs)
+    want = lo.quantize_rows(f64(s) * f64(w))[0]
+    assert (f64(q) == want).all()
+
+
+@pytest.mark.parametrize("xs,ws", [(1.0, 1e-34), (1.0, 1e-36), (1.0, 1e-38), (1e-18, 1e-30), (1e-3, 3e37),
+                                   (1e17, 1e30), (1e17, 1e-30), (1e-18, 1e35)])
+def test_forward_small_and_large(xs, ws):
+    """Blocks at and below the scale's floor, and outputs near the ends of fp32, from rows whose
+    products with the weights alone leave it.  2^-148: steps of subnormal numbers; a block
+    below the floor is divided by it to 1.2e-6 = 20 u."""
+    x, w = draw(1, 9, 1040, torch.float32, xs), draw(2, 1, 1040, torch.float32)[0].clamp(-2, 2) * ws
+    y, q = torch.empty_like(x), torch.empty(9, 1040, dtype=F8, device="cuda")
+    s = torch.empty(moe.scale_blocks(1040), 9, device="cuda")
+    moe.moe_rmsnorm(x, w, 0.0, y=y, y_q=q, y_scale=s)
+    want, _ = lo.rmsnorm(f64(x), f64(w), 0.0)
+    e = 36 * U * np.abs(want) + 2.0 ** -148
+    assert (np.abs(f64(y) - want) <= e).all()
+    sc, amax = f64(s), lo.quantize_rows(want)[1]
+    assert (np.abs(sc - amax) <= 40 * U * amax).all() and (sc >= 2.0 ** -126).all()
+    step = np.repeat(sc.T, 128, 1)[:, :1040]
+    assert (np.abs(f64(q) * step - want) <= (2.0 ** -4 * (1 + 8 * U)) * (np.abs(want) + e) + e + step * 2.0 ** -10).all()
