@@ -386,7 +386,8 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const void* w_gate
  *  residual_out [rows, d] out or NULL: r.  May be x or residual itself.
  *  y            [rows, d] out or NULL
  *  y_q, y_scale [rows, d] e4m3 and [ceil(d/128), rows] fp32 out, or both NULL: y in 8 bits,
- *               quantised from the fp32 values (not from the rounded y); d % 16 == 0
+ *               quantised from fp32 (not from the rounded y): rstd cancels in 448 y / max|y|,
+ *               so q is that of r * weight, exact for 16-bit inputs; d % 16 == 0
  *  rstd         [rows] fp32 out or NULL (the backward needs it)
  * d a multiple of 8, at most 16384; at least one output; eps >= 0.  rows == 0 launches
  * nothing.  r^2 must not overflow fp32 (|r| below 1e18 or so), as usual for this norm. */

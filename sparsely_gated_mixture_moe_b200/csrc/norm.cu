@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(512)
                                                       : 1.0f + rstd * 0.0f;
   // of u, a little below what y's floor is there: then the scale is y's floor itself
   const float floor = kAmaxFloor * 0.999999f * rcp_ftz(rest);
-  // 16 lanes hold a block; its i-th lane keeps the i-th vector's maximum and stores its scale, so
-  // that one division serves all vectors (98.4 us instead of 100.5 on 65536 x 1024).
+  // 16 lanes hold a block; the i-th of them keeps the maximum of the i-th vectors and stores their
+  // scale, so that one division serves all (99.4 us instead of 100.5 on 65536 x 1024).
   const int lane16 = threadIdx.x & 15;
   float mine = 0.0f;
 #pragma unroll
@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(512)
       load8(weight + col, w);
 #pragma unroll
       for (int j = 0; j < 8; j += 2)
-        f2_unpack(f2_mul(f2_mul(f2_pack(v[i][j], v[i][j + 1]), f2_splat(power)), f2_pack(w[j], w[j + 1])), v[i][j],
-                  v[i][j + 1]);
+        f2_unpack(f2_mul(f2_mul(f2_pack(v[i][j], v[i][j + 1]), f2_splat(power)),
+                         f2_pack(w[j], w[j + 1])),
+                  v[i][j], v[i][j + 1]);
       if (y != nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2)
@@ -128,13 +129,13 @@ __global__ void __launch_bounds__(512)
       }
     }
     if (q != nullptr) {
-      const float m = max_nan(amax_half_warp(amax8(v[i])), floor);
-      if (lane16 == i) mine = m;
+      const float m = max_nan(amax_half_warp(amax8(v[i])), floor), top = m * rest;
+      if (lane16 == i) mine = top;
       if (in) {
         // 448 u / m, rounded once: what the approximate quotient lacks is added back.  (A quarter
-        // of m has a reciprocal in the normal range.)
+        // of m has a reciprocal in the normal range; top - top is NaN where y overflows.)
         const float inv = rcp_ftz(m * 0.25f), hi = (0.25f * kE4m3Max) * inv;
-        const float lo = fmaf(-hi, m, kE4m3Max) * (0.25f * inv);
+        const float lo = fmaf(fmaf(-hi, m, kE4m3Max), 0.25f * inv, top - top);
         uint32_t b[2];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(512)
   }
   const int mycol = col0 - lane16 * 8 + lane16 * step;
   if (q != nullptr && live && lane16 < VEC && mycol < d)
-    scale[static_cast<int64_t>(mycol / kScaleBlock) * rows + row] = block_scale(max_nan(mine * rest, kAmaxFloor));
+    scale[static_cast<int64_t>(mycol / kScaleBlock) * rows + row] = block_scale(max_nan(mine, kAmaxFloor));
 }
 
 // Each block walks rows blockIdx.x * rows-per-block, + gridDim.x * ..., its threads keeping

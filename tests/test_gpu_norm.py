@@ -231,3 +231,16 @@ def test_forward_small_and_large(xs, ws):
     assert (np.abs(sc - amax) <= 40 * U * amax).all() and (sc >= 2.0 ** -126).all()
     step = np.repeat(sc.T, 128, 1)[:, :1040]
     assert (np.abs(f64(q) * step - want) <= (2.0 ** -4 * (1 + 8 * U)) * (np.abs(want) + e) + e + step * 2.0 ** -10).all()
+
+
+def test_forward_outputs_beyond_fp32():
+    """100 ones of 256 values: rstd = 1.6, and y = 1.6 w overflows where w alone does not.  The
+    block reads back as NaN throughout, its neighbour as zeros."""
+    x = torch.zeros(2, 256, device="cuda")
+    x[:, :100] = 1.0
+    w = torch.full((256,), 3e38, device="cuda")
+    y, q, s = torch.empty_like(x), torch.empty(2, 256, dtype=F8, device="cuda"), torch.empty(2, 2, device="cuda")
+    moe.moe_rmsnorm(x, w, 0.0, y=y, y_q=q, y_scale=s)
+    assert torch.isinf(y[:, :100]).all() and not y[:, 100:].any()
+    back = lo.rows_value(f64(q), f64(s))
+    assert np.isnan(back[:, :128]).all() and (back[:, 128:] == 0).all()
