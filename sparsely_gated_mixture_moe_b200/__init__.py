@@ -609,6 +609,7 @@ class MoELayerFP8:
         elif residual is not None:
             raise ValueError("a residual is added by the norm: weights hold none")
         else:
+            _need("x", x, self.n_q.shape, torch.bfloat16, _here("x", x))
             moe_quantize_rows_fp8(x, self.n_q, self.n_scale, stream=stream)
             rows = x
         moe_route(cfg, rows, w["w_gate"], self.topk_idx, self.topk_gate, ws, w_noise=w["w_noise"],

@@ -134,3 +134,16 @@ def test_trained_through_the_norm():
     num = (loss(R + h * v) - loss(R - h * v)) / (2 * h)
     # rstd within 32 u of the formula's, as in the forward's test
     assert abs((H.f64(dx) * v).sum() - num) <= 1e-5 * np.abs(H.f64(dx) * v).sum()
+
+
+def test_layer_refuses_other_rows():
+    """Rows of another type, shape or device are refused, with a norm and without."""
+    for normed in (False, True):
+        inp, dev, cfg, weights, layer = layer_of(LAYERS["decode"], normed)
+        x = dev["x"]
+        for bad in (x.float(), x[:4], x[:, :128].contiguous(), x.cpu(), x.t().contiguous().t()):
+            with pytest.raises(ValueError):
+                layer.forward(bad)
+        if not normed:
+            with pytest.raises(ValueError):
+                layer.forward(x, residual=x)
